@@ -133,8 +133,7 @@ int check_current_device() {
 int record_cuda_error(cudaError_t e) { return record_cuda(e); }
 
 namespace {
-bool encode_map(CUtensorMap* map, CUtensorMapDataType dtype, int elem_bytes, const void* base, int cols, int rows,
-                int outer, int box_cols, int box_rows) {
+bool load_encode() {
   std::call_once(g_encode_once, [] {
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -142,7 +141,12 @@ bool encode_map(CUtensorMap* map, CUtensorMapDataType dtype, int elem_bytes, con
         q == cudaDriverEntryPointSuccess)
       g_encode = reinterpret_cast<EncodeTiledFn>(fn);
   });
-  if (!g_encode) return false;
+  return g_encode != nullptr;
+}
+
+bool encode_map(CUtensorMap* map, CUtensorMapDataType dtype, int elem_bytes, const void* base, int cols, int rows,
+                int outer, int box_cols, int box_rows) {
+  if (!load_encode()) return false;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
                         static_cast<cuuint64_t>(outer)};
   cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols) * elem_bytes,
@@ -158,6 +162,48 @@ bool encode_map(CUtensorMap* map, CUtensorMapDataType dtype, int elem_bytes, con
 
 bool encode_tile_map(CUtensorMap* map, const void* base, int cols, int rows, int outer, int box_rows) {
   return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, cols, rows, outer, 64, box_rows);
+}
+
+bool encode_bf16_map(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+                     const uint32_t* box) {
+  if (!load_encode()) return false;
+  cuuint64_t d[5], st[4];
+  cuuint32_t b[5], es[5];
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    b[i] = box[i];
+    es[i] = 1;
+    // A dimension of one element is never stepped along: any valid stride.
+    if (i > 0) st[i - 1] = dims[i] == 1 ? dims[0] * 2 : strides[i - 1];
+  }
+  return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), d, st, b, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_rows_map(CUtensorMap* map, const Rows& x, int T, int H, int d, int box_rows) {
+  const uint64_t dims[3] = {static_cast<uint64_t>(d), static_cast<uint64_t>(T), static_cast<uint64_t>(H)};
+  const uint64_t st[2] = {static_cast<uint64_t>(x.ts) * 2, static_cast<uint64_t>(x.hs) * 2};
+  const uint32_t box[3] = {64, static_cast<uint32_t>(box_rows), 1};
+  return encode_bf16_map(map, x.p, 3, dims, st, box);
+}
+
+bool encode_group_map(CUtensorMap* map, const Rows& x, int T, int Hkv, int r, int d, int tokens) {
+  const uint64_t dims[4] = {static_cast<uint64_t>(d), static_cast<uint64_t>(r), static_cast<uint64_t>(T),
+                            static_cast<uint64_t>(Hkv)};
+  const uint64_t st[3] = {static_cast<uint64_t>(x.hs) * 2, static_cast<uint64_t>(x.ts) * 2,
+                          static_cast<uint64_t>(x.hs) * 2 * r};
+  const uint32_t box[4] = {64, static_cast<uint32_t>(r), static_cast<uint32_t>(tokens), 1};
+  return encode_bf16_map(map, x.p, 4, dims, st, box);
+}
+
+bool encode_pages_map(CUtensorMap* map, const Pages& x, int n_pages, int Hkv, int page, int d, int box_rows) {
+  const uint64_t dims[4] = {static_cast<uint64_t>(d), static_cast<uint64_t>(page), static_cast<uint64_t>(Hkv),
+                            static_cast<uint64_t>(n_pages)};
+  const uint64_t st[3] = {static_cast<uint64_t>(x.ss) * 2, static_cast<uint64_t>(x.hs) * 2,
+                          static_cast<uint64_t>(x.ps) * 2};
+  const uint32_t box[4] = {64, static_cast<uint32_t>(box_rows), 1, 1};
+  return encode_bf16_map(map, x.p, 4, dims, st, box);
 }
 
 bool encode_f32_tile_map(CUtensorMap* map, const void* base, int cols, int rows, int outer, int box_cols,
@@ -358,6 +404,8 @@ const char* fa_status_string(int status) {
       return t_cuda_msg;
     case FA_ERR_TIMEOUT:
       return "a kernel wait ran past the watchdog budget and the kernel gave up";
+    case FA_ERR_DATA:
+      return "sequence offsets, lengths or page numbers in device memory are out of range";
     default:
       return "unknown status";
   }
@@ -377,10 +425,220 @@ int fa_check_device_error(void* stream) {
   if (e != cudaSuccess) return record_cuda(e);
   e = cudaDeviceSynchronize();
   if (e != cudaSuccess) return record_cuda(e);
-  return FA_ERR_TIMEOUT;
+  return (word & ~kErrData) != 0 ? FA_ERR_TIMEOUT : FA_ERR_DATA;
 }
 
 void fa_set_watchdog_ns(uint64_t ns) { g_budget_ns.store(ns < 1000000ull ? 1000000ull : ns); }
+
+// ------------------------------------------ packed sequences, paged cache
+
+// At most this many CTAs share the work that is cut along the keys (one per
+// SM of a B200); the workspace sizes depend on it.
+static constexpr int kShareCtas = 148;
+
+// Strides: whole 16-byte pieces, positive where there is more than one
+// element (a stride of zero would make rows share memory), and below TMA's
+// 2^40 bytes.
+static bool stride_ok(long long st, long long count) {
+  return count <= 1 || (st > 0 && st % 8 == 0 && st < (1LL << 39));
+}
+static bool rows_ok(const fa_rows* x, int T, int H) {
+  return x && x->data && aligned16(x->data) && stride_ok(x->token_stride, T) && stride_ok(x->head_stride, H);
+}
+static bool pages_ok(const fa_pages* x, int n_pages, int H, int page) {
+  return x && x->data && aligned16(x->data) && stride_ok(x->page_stride, n_pages) && stride_ok(x->head_stride, H) &&
+         stride_ok(x->slot_stride, page);
+}
+static Rows as_rows(const fa_rows* x) { return x ? Rows{x->data, x->token_stride, x->head_stride} : Rows{}; }
+static Pages as_pages(const fa_pages* x) { return Pages{x->data, x->page_stride, x->head_stride, x->slot_stride}; }
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+static int check_seqs(int S, int T, int Hq, int Hkv, int d, int causal, float scale) {
+  if (S < 0 || T < 0 || Hq <= 0 || Hkv <= 0) return FA_ERR_INVALID_ARGUMENT;
+  if (causal != 0 && causal != 1) return FA_ERR_INVALID_ARGUMENT;
+  if (!std::isfinite(scale) || !(scale > 0.f)) return FA_ERR_INVALID_ARGUMENT;
+  if ((d != 64 && d != 128) || Hq % Hkv != 0 || Hq / Hkv > 128) return FA_ERR_UNSUPPORTED;
+  if (Hq > (1 << 16) || T > (1 << 30) || S > (1 << 24)) return FA_ERR_UNSUPPORTED;
+  // CTAs of one launch: (units of at least one token) * KV heads.
+  if ((static_cast<long long>(T) + S + 4 * kShareCtas) * Hkv > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+
+static int check_cache(int n_pages, int page_size, int max_pages, int max_q) {
+  if (n_pages < 0 || page_size <= 0 || max_pages < 0 || max_q < 0) return FA_ERR_INVALID_ARGUMENT;
+  if (page_size % 8 != 0 || page_size > (1 << 20)) return FA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(max_pages) * page_size > (1 << 30)) return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+
+size_t fa_packed_fwd_workspace_bytes(int S, int T, int Hq, int Hkv, int d) {
+  if (check_seqs(S, T, Hq, Hkv, d, 0, 1.f) != FA_OK) return 0;
+  return packed_fwd_workspace_bytes(SeqShape{S, T, nullptr, Hq, Hkv, d, 0, 1.f}, nullptr, kShareCtas);
+}
+
+int fa_packed_fwd(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa_rows* o, const fa_rows* o_resid,
+                  float* lse, const int* cu_seqlens, int S, int T, int Hq, int Hkv, int d, int causal, float scale,
+                  void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_seqs(S, T, Hq, Hkv, d, causal, scale);
+  if (rc != FA_OK) return rc;
+  if (S == 0 || T == 0) return FA_OK;
+  if (!rows_ok(q, T, Hq) || !rows_ok(k, T, Hkv) || !rows_ok(v, T, Hkv) || !rows_ok(o, T, Hq) ||
+      (o_resid && !rows_ok(o_resid, T, Hq)) || !lse || !aligned4(lse) || !cu_seqlens || !aligned4(cu_seqlens) ||
+      !workspace || !aligned16(workspace))
+    return FA_ERR_INVALID_ARGUMENT;
+  const SeqShape s{S, T, cu_seqlens, Hq, Hkv, d, causal, scale};
+  if (workspace_bytes < packed_fwd_workspace_bytes(s, nullptr, kShareCtas)) return FA_ERR_INVALID_ARGUMENT;
+  DevState* st = nullptr;
+  if ((rc = device_state(&st)) != FA_OK) return rc;
+  const int ctas = st->sms < kShareCtas ? st->sms : kShareCtas;
+  cudaError_t e = launch_packed_fwd(s, nullptr, as_rows(q), as_rows(o), as_rows(o_resid), as_rows(k), as_rows(v),
+                                    Pages{}, Pages{}, lse, workspace, ctas, make_ctl(st),
+                                    static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : record_cuda(e);
+}
+
+size_t fa_packed_bwd_workspace_bytes(int S, int T, int Hq, int Hkv, int d) {
+  if (check_seqs(S, T, Hq, Hkv, d, 0, 1.f) != FA_OK) return 0;
+  return packed_bwd_workspace_bytes(SeqShape{S, T, nullptr, Hq, Hkv, d, 0, 1.f});
+}
+
+int fa_packed_bwd(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa_rows* o, const fa_rows* o_resid,
+                  const fa_rows* dout, const float* lse, const fa_rows* dq, const fa_rows* dk, const fa_rows* dv,
+                  const int* cu_seqlens, int S, int T, int Hq, int Hkv, int d, int causal, float scale,
+                  void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_seqs(S, T, Hq, Hkv, d, causal, scale);
+  if (rc != FA_OK) return rc;
+  if (S == 0 || T == 0) return FA_OK;
+  if (!rows_ok(q, T, Hq) || !rows_ok(k, T, Hkv) || !rows_ok(v, T, Hkv) || !rows_ok(o, T, Hq) ||
+      (o_resid && !rows_ok(o_resid, T, Hq)) || !rows_ok(dout, T, Hq) || !rows_ok(dq, T, Hq) || !rows_ok(dk, T, Hkv) ||
+      !rows_ok(dv, T, Hkv) || !lse || !aligned4(lse) || !cu_seqlens || !aligned4(cu_seqlens) || !workspace ||
+      !aligned16(workspace))
+    return FA_ERR_INVALID_ARGUMENT;
+  const SeqShape s{S, T, cu_seqlens, Hq, Hkv, d, causal, scale};
+  if (workspace_bytes < packed_bwd_workspace_bytes(s)) return FA_ERR_INVALID_ARGUMENT;
+  DevState* st = nullptr;
+  if ((rc = device_state(&st)) != FA_OK) return rc;
+  cudaError_t e = launch_packed_bwd(s, as_rows(q), as_rows(k), as_rows(v), as_rows(o), as_rows(o_resid), as_rows(dout),
+                                    lse, as_rows(dq), as_rows(dk), as_rows(dv), workspace, make_ctl(st),
+                                    static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : record_cuda(e);
+}
+
+size_t fa_paged_fwd_workspace_bytes(int S, int T, int max_q, int Hq, int Hkv, int d, int page_size, int max_pages) {
+  if (check_seqs(S, T, Hq, Hkv, d, 0, 1.f) != FA_OK || check_cache(0, page_size, max_pages, max_q) != FA_OK) return 0;
+  const SeqShape s{S, T, nullptr, Hq, Hkv, d, 0, 1.f};
+  CacheShape c{0, page_size, max_pages, nullptr, nullptr, 0, max_q < T ? max_q : T};
+  return paged_few_rows(s, c) ? paged_few_workspace_bytes(s, c, kShareCtas)
+                              : packed_fwd_workspace_bytes(s, &c, kShareCtas);
+}
+
+int fa_paged_fwd(const fa_rows* q, const fa_pages* k_pages, const fa_pages* v_pages, const fa_rows* o, float* lse,
+                 int n_pages, int page_size, const int* block_table, int64_t table_stride, int max_pages,
+                 const int* seq_lens, const int* cu_seqlens, int S, int T, int max_q, int Hq, int Hkv, int d,
+                 int causal, float scale, void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_seqs(S, T, Hq, Hkv, d, causal, scale);
+  if (rc != FA_OK || (rc = check_cache(n_pages, page_size, max_pages, max_q)) != FA_OK) return rc;
+  if (!cu_seqlens && S != T) return FA_ERR_INVALID_ARGUMENT;
+  if (S == 0 || T == 0) return FA_OK;
+  if (n_pages == 0 || max_pages == 0 || max_q == 0) return FA_ERR_INVALID_ARGUMENT;
+  if (!rows_ok(q, T, Hq) || !rows_ok(o, T, Hq) || !pages_ok(k_pages, n_pages, Hkv, page_size) ||
+      !pages_ok(v_pages, n_pages, Hkv, page_size) || !lse || !aligned4(lse) || !block_table || !aligned4(block_table) ||
+      table_stride < (S > 1 ? max_pages : 0) || !seq_lens || !aligned4(seq_lens) || !aligned4(cu_seqlens) ||
+      !workspace || !aligned16(workspace))
+    return FA_ERR_INVALID_ARGUMENT;
+  const SeqShape s{S, T, cu_seqlens, Hq, Hkv, d, causal, scale};
+  const CacheShape c{n_pages, page_size, max_pages, seq_lens, block_table, table_stride, max_q < T ? max_q : T};
+  const bool few = paged_few_rows(s, c);
+  const size_t need = few ? paged_few_workspace_bytes(s, c, kShareCtas) : packed_fwd_workspace_bytes(s, &c, kShareCtas);
+  if (workspace_bytes < need) return FA_ERR_INVALID_ARGUMENT;
+  DevState* st = nullptr;
+  if ((rc = device_state(&st)) != FA_OK) return rc;
+  const int ctas = st->sms < kShareCtas ? st->sms : kShareCtas;
+  cudaError_t e =
+      few ? launch_paged_few(s, c, as_rows(q), as_rows(o), as_pages(k_pages), as_pages(v_pages), lse, workspace, ctas,
+                             make_ctl(st), static_cast<cudaStream_t>(stream))
+          : launch_packed_fwd(s, &c, as_rows(q), as_rows(o), Rows{}, Rows{}, Rows{}, as_pages(k_pages),
+                              as_pages(v_pages), lse, workspace, ctas, make_ctl(st), static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : record_cuda(e);
+}
+
+// Checks the rotation's arguments and fills its shape.
+static int rope_shape(RopeShape* s, int T, int Hq, int Hkv, int d, const int* positions, const double* inv_freq,
+                      const int* sections, int n_sections, int interleaved, int inverse, bool need_positions) {
+  if (T < 0 || Hq < 0 || Hkv < 0 || (interleaved != 0 && interleaved != 1) || (inverse != 0 && inverse != 1))
+    return FA_ERR_INVALID_ARGUMENT;
+  if (n_sections < 0 || (n_sections > 0 && !sections)) return FA_ERR_INVALID_ARGUMENT;
+  if ((d != 64 && d != 128) || n_sections > 4) return FA_ERR_UNSUPPORTED;
+  if (Hq > (1 << 16) || Hkv > (1 << 16) || T > (1 << 30)) return FA_ERR_UNSUPPORTED;
+  *s = RopeShape{};
+  int pairs = 0;
+  for (int i = 0; i < n_sections; ++i) {
+    if (sections[i] <= 0 || sections[i] > d) return FA_ERR_INVALID_ARGUMENT;
+    pairs += sections[i];
+    s->section_end[i] = pairs;
+  }
+  if (2 * pairs > d) return FA_ERR_INVALID_ARGUMENT;
+  if (pairs % 8 != 0) return FA_ERR_UNSUPPORTED;
+  if (pairs > 0 && (!inv_freq || (reinterpret_cast<uintptr_t>(inv_freq) & 7u))) return FA_ERR_INVALID_ARGUMENT;
+  if (pairs > 0 && ((need_positions && !positions) || !aligned4(positions))) return FA_ERR_INVALID_ARGUMENT;
+  s->T = T;
+  s->Hq = Hq;
+  s->Hkv = Hkv;
+  s->d = d;
+  s->pairs = pairs;
+  s->interleaved = interleaved;
+  s->sign = inverse ? -1.f : 1.f;
+  s->positions = positions;
+  s->inv_freq = inv_freq;
+  s->n_sections = n_sections;
+  return FA_OK;
+}
+
+int fa_rope(const fa_rows* q, const fa_rows* k, const fa_rows* q_out, const fa_rows* k_out, const int* positions,
+            const double* inv_freq, const int* sections, int n_sections, int T, int Hq, int Hkv, int d,
+            int interleaved, int inverse, void* stream) {
+  RopeShape s;
+  int rc = rope_shape(&s, T, Hq, Hkv, d, positions, inv_freq, sections, n_sections, interleaved, inverse, true);
+  if (rc != FA_OK) return rc;
+  if (s.pairs == 0 || Hq + Hkv == 0) return FA_ERR_INVALID_ARGUMENT;
+  if (T == 0) return FA_OK;
+  if ((Hq > 0 && (!rows_ok(q, T, Hq) || !rows_ok(q_out, T, Hq))) ||
+      (Hkv > 0 && (!rows_ok(k, T, Hkv) || !rows_ok(k_out, T, Hkv))))
+    return FA_ERR_INVALID_ARGUMENT;
+  DevState* st = nullptr;
+  if ((rc = device_state(&st)) != FA_OK) return rc;
+  cudaError_t e = launch_rope(s, as_rows(Hq ? q : nullptr), as_rows(Hkv ? k : nullptr), as_rows(Hq ? q_out : nullptr),
+                              as_rows(Hkv ? k_out : nullptr), static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : record_cuda(e);
+}
+
+int fa_paged_append(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa_rows* q_out,
+                    const fa_pages* k_pages, const fa_pages* v_pages, int n_pages, int page_size,
+                    const int* block_table, int64_t table_stride, int max_pages, const int* seq_lens,
+                    const int* cu_seqlens, int S, int T, const int* positions, const double* inv_freq,
+                    const int* sections, int n_sections, int Hq, int Hkv, int d, int interleaved, void* stream) {
+  if (S < 0 || Hkv <= 0) return FA_ERR_INVALID_ARGUMENT;
+  RopeShape s;
+  int rc = rope_shape(&s, T, Hq, Hkv, d, positions, inv_freq, sections, n_sections, interleaved, 0, n_sections > 1);
+  if (rc != FA_OK || (rc = check_cache(n_pages, page_size, max_pages, 0)) != FA_OK) return rc;
+  if (S > (1 << 24)) return FA_ERR_UNSUPPORTED;
+  if (!cu_seqlens && S != T) return FA_ERR_INVALID_ARGUMENT;
+  if (S == 0 || T == 0) return FA_OK;
+  if (n_pages == 0 || max_pages == 0) return FA_ERR_INVALID_ARGUMENT;
+  if ((Hq > 0 && (!rows_ok(q, T, Hq) || !rows_ok(q_out, T, Hq))) || !rows_ok(k, T, Hkv) || !rows_ok(v, T, Hkv) ||
+      !pages_ok(k_pages, n_pages, Hkv, page_size) || !pages_ok(v_pages, n_pages, Hkv, page_size) || !block_table ||
+      !aligned4(block_table) || table_stride < (S > 1 ? max_pages : 0) || !seq_lens || !aligned4(seq_lens) ||
+      !aligned4(cu_seqlens))
+    return FA_ERR_INVALID_ARGUMENT;
+  DevState* st = nullptr;
+  if ((rc = device_state(&st)) != FA_OK) return rc;
+  const SeqShape seq{S, T, cu_seqlens, Hq, Hkv, d, 0, 1.f};
+  const CacheShape c{n_pages, page_size, max_pages, seq_lens, block_table, table_stride, T};
+  cudaError_t e = launch_paged_append(s, seq, c, as_rows(Hq ? q : nullptr), as_rows(k), as_rows(v),
+                                      as_rows(Hq ? q_out : nullptr), as_pages(k_pages), as_pages(v_pages), st->err,
+                                      static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : record_cuda(e);
+}
 
 // Test hook, declared in include/fa_test.h: selects a deliberate stall
 // (1 = the forward producer never loads the first K tile) so that the

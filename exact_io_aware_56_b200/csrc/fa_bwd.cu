@@ -31,6 +31,14 @@
 //             dK_j (times scale) and dV_j are written once.
 //   bwd_post  dq = bf16(scale * accumulator).
 //
+// Packed sequences (VAR): rows [cu[b], cu[b+1]) of [T][H][d] views are
+// sequence b. The (sequence, key tile) units come from a list (fa_plan.cuh),
+// longest first, times the KV heads. A tile that reaches past its sequence
+// holds the next sequence's rows, which may be anything: warp 10 zeroes them
+// in shared memory (K, V once; Q and dO of each head's last tile), after
+// which they are what rows past N are to the equal-length form, where TMA
+// fills zeros. dK and dV of such a tile are stored row by row.
+//
 // Warp roles of bwd_main (512 threads):
 //   warps 0-3   softmax-gradient warpgroup for even query tiles (buffer 0),
 //   warps 4-7   the same for odd tiles (buffer 1): thread = key row; writes
@@ -42,7 +50,8 @@
 //   warp 9      tensor-memory owner and MMA issuer (the whole warp runs the
 //               issue loop so operand descriptors stay warp-uniform; one
 //               elected lane issues).
-//   warps 10-11 idle (keep the third warpgroup whole).
+//   warp 10     VAR: zeroes rows behind the sequence's end; else idle.
+//   warp 11     idle (keeps the third warpgroup whole).
 //   warps 12-15 dQ warpgroup: thread = column c of dQ; reads dQ_i^T out of
 //               tensor memory, releases it and issues the reductions;
 //               epilogue stores dK.
@@ -59,6 +68,7 @@
 #include <math_constants.h>
 
 #include "fa_internal.h"
+#include "fa_plan.cuh"
 #include "sm100.cuh"
 
 
@@ -70,6 +80,7 @@ constexpr int kQT = 64;    // queries per query tile
 constexpr int kThreads = 512;
 constexpr int kProducerWarp = 8;
 constexpr int kMmaWarp = 9;
+constexpr int kFixWarp = 10;
 constexpr int kDqWarp0 = 12;
 constexpr int kQStages = 3;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -88,7 +99,7 @@ struct BwdCfg {
   static constexpr int kOffDS = kOffDO + kQStages * kQTile;
   static constexpr int kOffLD = kOffDS + 2 * kDSTile;      // [stage] L2[64], D[64]
   static constexpr int kOffBar = kOffLD + kQStages * 2 * kQT * 4;
-  static constexpr int kUsed = kOffBar + 256;
+  static constexpr int kUsed = kOffBar + 320;
   static constexpr int kSmemBytes = (kUsed + 1024 <= 232448) ? kUsed + 1024 : 232448;
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kColS = 0, kColDP = 128, kColDV = 256, kColDK = 256 + D;
@@ -106,6 +117,11 @@ struct BwdArgs {
   int window;  // left window (a huge value when there is none), mask kind 2
   int prefix;  // prefix length, mask kind 2
   float scale, scale_log2;
+  // Packed sequences only (N is then the rows T).
+  const PlanHeader* head;
+  const PlanItem* items;
+  const int* cu;
+  Rows dk, dv;
   LaunchCtl ctl;
 };
 
@@ -115,10 +131,11 @@ struct BwdBars {
   uint64_t s_full[2], dp_full[2], p_ready[2], ds_free[2], dq_full[2], dq_empty[2];
   uint64_t acc_final, drain;
   uint64_t epi_dv, epi_dk;  // output staging: all rows of dV / dK written to shared memory
+  uint64_t kv_land, q_land[kQStages];  // packed: copies of tiles whose last rows are to be zeroed
   uint32_t tmem_base;
   int abort;
 };
-static_assert(sizeof(BwdBars) <= 256, "barrier block exceeds its shared-memory reservation");
+static_assert(sizeof(BwdBars) <= 320, "barrier block exceeds its shared-memory reservation");
 
 __device__ __forceinline__ void fence_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -128,9 +145,24 @@ __device__ __forceinline__ void red_add_f32(float* addr, float v) {
   asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(addr), "f"(v) : "memory");
 }
 
+// Stores `rows` rows of a staged tile (64-column boxes of 128-byte rows,
+// 128-byte swizzle) to tokens row0.. of head h, by `threads` threads.
+template <int D>
+__device__ __forceinline__ void store_rows_t(const uint8_t* tile, int box_bytes, int rows, const Rows& out, int row0,
+                                             int h, int tid, int threads) {
+  constexpr int kPieces = D / 8;  // 16-byte pieces per row
+  for (int e = tid; e < rows * kPieces; e += threads) {
+    const int rw = e / kPieces, c = e % kPieces;
+    const uint4 v = *reinterpret_cast<const uint4*>(tile + (c / 8) * box_bytes + rw * 128 + (((c % 8) ^ (rw & 7)) << 4));
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out.p) + (static_cast<long long>(row0) + rw) * out.ts +
+                              h * out.hs + c * 8) = v;
+  }
+}
+
 // MASK: 0 none, 1 causal, 2 causal with a left window and/or a prefix
 // (key j visible to query i iff (j <= i and i - j <= window) or j < prefix).
-template <int D, int MASK>
+// VAR: packed sequences (masks 0 and 1).
+template <int D, int MASK, bool VAR = false>
 __global__ void __launch_bounds__(kThreads, 1)
     bwd_main_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
@@ -142,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t pad = (1024u - (raw_addr & 1023u)) & 1023u;
   if (pad + C::kUsed > static_cast<uint32_t>(C::kSmemBytes)) {
     // Not enough room to align the tiles: report instead of overrunning.
-    if (threadIdx.x == 0) atomicOr(a.ctl.err, 2u);
+    if (threadIdx.x == 0) atomicOr(a.ctl.err, kErrAlign);
     return;
   }
   uint8_t* smem = smem_raw + pad;
@@ -158,7 +190,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   // tiles stay in L2 while the resident CTAs sweep them); within a group the
   // longest units (smallest j when causal) come first.
   int bkv, j;
-  if (MASK == 1 && a.band > 0) {
+  int base = 0, N = a.N;  // packed: the sequence's first row and its length
+  int nq = a.nq;
+  if constexpr (VAR) {
+    static_assert(MASK != 2, "packed sequences: no mask or causal");
+    pdl_wait();  // the plan and the D_i are written
+    const int item_no = blockIdx.x / a.Hkv;
+    if (item_no >= a.head->items) return;
+    const PlanItem item = a.items[item_no];
+    bkv = blockIdx.x - item_no * a.Hkv;
+    j = item.tok0 / kKT;
+    base = a.cu[item.seq];
+    N = a.cu[item.seq + 1] - base;
+    nq = (N + kQT - 1) / kQT;
+  } else if (MASK == 1 && a.band > 0) {
     // Bands of a.band key tiles, longest band first; within a band,
     // KV-head-major with the key tiles of a head adjacent, so that the
     // resident CTAs share the dQ accumulator, Q and dO of a few heads.
@@ -177,19 +222,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     j = rem / gsize;
   }
   const int r = a.Hq / a.Hkv;
-  const int b = bkv / a.Hkv;
-  const int g = bkv % a.Hkv;
+  const int b = VAR ? 0 : bkv / a.Hkv;
+  const int g = VAR ? bkv : bkv % a.Hkv;
   // Query tiles [i0, i0 + nqi) that see some key of tile j: all of them
   // without a mask or when the tile holds a prefix key; otherwise from the
   // tile's first key on (causal) up to its last key plus the window.
-  int i0 = 0, i1 = a.nq;
+  int i0 = 0, i1 = nq;
   if (MASK == 1) i0 = 2 * j;
   if (MASK == 2 && j * kKT >= a.prefix) {
     i0 = 2 * j;
     const long long last = static_cast<long long>(j) * kKT + kKT - 1 + a.window;
     i1 = static_cast<int>(min(static_cast<long long>(a.nq), last / kQT + 1));
   }
-  const int nqi = i1 - i0;             // query tiles per head
+  const int nqi = i1 - i0;             // query tiles per head (the last ends at nq)
   const int n_it = r * nqi;            // (head, query tile) iterations
 
   if (threadIdx.x == 0) {
@@ -205,6 +250,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars->ds_free[x], 1);
       mbar_init(&bars->dq_full[x], 1);
       mbar_init(&bars->dq_empty[x], 128);
+    }
+    if constexpr (VAR) {
+      mbar_init(&bars->kv_land, 1);
+      for (int s = 0; s < kQStages; ++s) mbar_init(&bars->q_land[s], 1);
     }
     mbar_init(&bars->acc_final, 1);
     mbar_init(&bars->drain, 1);
@@ -236,15 +285,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < kQStages; ++s) q_last[s] = -1;
     bool kv_issued = false;
     bool ok = true;
+    // Packed: uses of q_land[s] so far; q_last[s] is -1 after such a use.
+    int land_uses[kQStages];
+#pragma unroll
+    for (int s = 0; s < kQStages; ++s) land_uses[s] = 0;
+    const bool kv_tail = VAR && (j + 1) * kKT > N;
     if (lane == 0) {
       tma_prefetch_desc(&tmQ);
       tma_prefetch_desc(&tmK);
       tma_prefetch_desc(&tmV);
       tma_prefetch_desc(&tmDO);
-      mbar_arrive_expect_tx(&bars->kv_full, 2 * C::kKTile);
+      uint64_t* kv_bar = kv_tail ? &bars->kv_land : &bars->kv_full;
+      mbar_arrive_expect_tx(kv_bar, 2 * C::kKTile);
       for (int x = 0; x < D / 64; ++x) {
-        tma_load_3d(&tmK, &bars->kv_full, smem + C::kOffK + x * C::kKBox, x * 64, j * kKT, bkv);
-        tma_load_3d(&tmV, &bars->kv_full, smem + C::kOffV + x * C::kKBox, x * 64, j * kKT, bkv);
+        tma_load_3d(&tmK, kv_bar, smem + C::kOffK + x * C::kKBox, x * 64, base + j * kKT, bkv);
+        tma_load_3d(&tmV, kv_bar, smem + C::kOffV + x * C::kKBox, x * 64, base + j * kKT, bkv);
       }
       kv_issued = true;
     }
@@ -266,27 +321,71 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int e = 0; e < kQT / 32; ++e) {
         const int rr = e * 32 + lane;
         const int row = i * kQT + rr;
-        const bool in = row < a.N;
-        const size_t idx = static_cast<size_t>(bh) * a.N + row;
+        const bool in = row < N;
+        const size_t idx = static_cast<size_t>(bh) * a.N + base + row;
         l2[rr] = in ? a.lse[idx] * kLog2e : CUDART_INF_F;
         dd[rr] = in ? a.dsum[idx] : 0.f;
       }
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive_expect_tx(&bars->q_full[s], 2 * C::kQTile);
+        // Packed: the fixer hands a tile with rows to zero on to q_full.
+        const bool tail = VAR && (i + 1) * kQT > N;
+        uint64_t* q_bar = tail ? &bars->q_land[s] : &bars->q_full[s];
+        mbar_arrive_expect_tx(q_bar, 2 * C::kQTile);
         for (int x = 0; x < D / 64; ++x) {
-          tma_load_3d(&tmQ, &bars->q_full[s], smem + C::kOffQ + s * C::kQTile + x * C::kQBox, x * 64, i * kQT,
-                      bh);
-          tma_load_3d(&tmDO, &bars->q_full[s], smem + C::kOffDO + s * C::kQTile + x * C::kQBox, x * 64, i * kQT,
-                      bh);
+          tma_load_3d(&tmQ, q_bar, smem + C::kOffQ + s * C::kQTile + x * C::kQBox, x * 64, base + i * kQT, bh);
+          tma_load_3d(&tmDO, q_bar, smem + C::kOffDO + s * C::kQTile + x * C::kQBox, x * 64, base + i * kQT, bh);
         }
-        q_last[s] = u;
+        if (VAR && tail) {
+          q_last[s] = -1;
+          land_uses[s] += 1;
+        } else {
+          q_last[s] = u;
+        }
       }
     }
     if (lane == 0) {
-      if (kv_issued) drain_bar(&bars->kv_full, 0, w);
-      for (int s = 0; s < kQStages; ++s)
+      if (kv_issued) drain_bar(kv_tail ? &bars->kv_land : &bars->kv_full, 0, w);
+      for (int s = 0; s < kQStages; ++s) {
         if (q_last[s] >= 0) drain_bar(&bars->q_full[s], q_last[s] & 1, w);
+        if (VAR && land_uses[s] > 0) drain_bar(&bars->q_land[s], (land_uses[s] - 1) & 1, w);
+      }
+    }
+  } else if (VAR && warp == kFixWarp) {
+    // ------------------------------------ rows behind the sequence's end
+    auto zero_rows = [&](uint8_t* tile, int rows, int first, int box_bytes) {
+      for (int x = 0; x < D / 64; ++x) {
+        uint4* box = reinterpret_cast<uint4*>(tile + x * box_bytes);
+        for (int e = first * 8 + lane; e < rows * 8; e += 32) box[e] = make_uint4(0, 0, 0, 0);
+      }
+    };
+    bool ok = true;
+    if ((j + 1) * kKT > N) {
+      ok = __all_sync(0xffffffffu, wait_bar(&bars->kv_land, 0, w));
+      if (ok) {
+        zero_rows(smem + C::kOffK, kKT, N - j * kKT, C::kKBox);
+        zero_rows(smem + C::kOffV, kKT, N - j * kKT, C::kKBox);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->kv_full);
+      }
+    }
+    // The last query tile of each head, when it is short: iterations
+    // nqi - 1, 2 nqi - 1, ...
+    if (nq * kQT > N) {
+      uint32_t land_par = 0;
+      for (int it = nqi - 1; ok && it < n_it; it += nqi) {
+        const int s = it % kQStages;
+        ok = __all_sync(0xffffffffu, wait_bar(&bars->q_land[s], (land_par >> s) & 1, w));
+        if (!ok) break;
+        land_par ^= 1u << s;
+        const int first = N - (nq - 1) * kQT;
+        zero_rows(smem + C::kOffQ + s * C::kQTile, kQT, first, C::kQBox);
+        zero_rows(smem + C::kOffDO + s * C::kQTile, kQT, first, C::kQBox);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->q_full[s]);
+      }
     }
   } else if (warp == kMmaWarp) {
     // ----------------------------------------------------------- MMA issue
@@ -449,6 +548,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!((key <= qg && qg - key <= a.window) || key < a.prefix)) p[e] = 0.f;
             }
           }
+          // Key rows behind the sequence (zeroed, so S = 0): e^-L of a row with
+          // a very negative L overflows, and inf * 0 would reach dQ. (When
+          // causal, the diagonal masks them.)
+          if (VAR && MASK == 0 && key >= N) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) p[e] = 0.f;
+          }
           float g0, g1, g2, g3;
           fsub2(g0, g1, __uint_as_float(dv[4 * y]), __uint_as_float(dv[4 * y + 1]), dq.x, dq.y);
           fsub2(g2, g3, __uint_as_float(dv[4 * y + 2]), __uint_as_float(dv[4 * y + 3]), dq.z, dq.w);
@@ -505,9 +611,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       fence_proxy_async_smem();
       mbar_arrive(&bars->epi_dv);
-      if (threadIdx.x == 0 && wait_bar(&bars->epi_dv, 0, w)) {
+      if (VAR && (j + 1) * kKT > N) {
+        // The tile's rows of this sequence, from the staged boxes, 16 bytes
+        // per thread and step.
+        if (__all_sync(0xffffffffu, wait_bar(&bars->epi_dv, 0, w)))
+          store_rows_t<D>(smem + C::kOffV, C::kKBox, N - j * kKT, a.dv, base + j * kKT, bkv, threadIdx.x, 256);
+      } else if (threadIdx.x == 0 && wait_bar(&bars->epi_dv, 0, w)) {
 #pragma unroll
-        for (int b = 0; b < D / 64; ++b) tma_store_3d(&tmDV, smem + C::kOffV + b * C::kKBox, b * 64, j * kKT, bkv);
+        for (int b = 0; b < D / 64; ++b) tma_store_3d(&tmDV, smem + C::kOffV + b * C::kKBox, b * 64, base + j * kKT, bkv);
         bulk_commit();
       }
       if (threadIdx.x == 0) bulk_wait_read<0>();
@@ -539,8 +650,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive(&bars->dq_empty[x]);
       if (m < D) {
         const int row0 = i * kQT;
-        float* col = a.dq_acc + (static_cast<size_t>(bh) * a.N + row0) * D + m;
-        const int rows = min(kQT, a.N - row0);
+        float* col = a.dq_acc + (static_cast<size_t>(bh) * a.N + base + row0) * D + m;
+        const int rows = min(kQT, N - row0);
         if (rows == kQT) {
 #pragma unroll
           for (int q = 0; q < 32; ++q) red_add_f32(col + static_cast<size_t>(q) * D, __uint_as_float(v0[q]));
@@ -579,9 +690,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_proxy_async_smem();
       mbar_arrive(&bars->epi_dk);
       const bool issuer = warp == kDqWarp0 && lane == 0;
-      if (issuer && wait_bar(&bars->epi_dk, 0, w)) {
+      if (VAR && (j + 1) * kKT > N) {
+        if (__all_sync(0xffffffffu, wait_bar(&bars->epi_dk, 0, w)))
+          store_rows_t<D>(smem + C::kOffK, C::kKBox, N - j * kKT, a.dk, base + j * kKT, bkv, m, 128);
+      } else if (issuer && wait_bar(&bars->epi_dk, 0, w)) {
 #pragma unroll
-        for (int b = 0; b < D / 64; ++b) tma_store_3d(&tmDK, smem + C::kOffK + b * C::kKBox, b * 64, j * kKT, bkv);
+        for (int b = 0; b < D / 64; ++b) tma_store_3d(&tmDK, smem + C::kOffK + b * C::kKBox, b * 64, base + j * kKT, bkv);
         bulk_commit();
       }
       if (issuer) bulk_wait_read<0>();
@@ -721,7 +835,171 @@ cudaError_t launch_bwd_t(const AttnShape& s, const CUtensorMap& tq, const CUtens
   return cudaGetLastError();
 }
 
+// D_i and the zeroed dQ accumulator of packed rows: one warp per (head, row),
+// rows outside [cu[0], cu[S]) left out. dsum and dq_acc are [Hq][T] and
+// [Hq][T][D].
+template <int D>
+__global__ void __launch_bounds__(256) packed_pre_kernel(Rows o, Rows resid, Rows dout, float* __restrict__ dsum,
+                                                         float* __restrict__ dq_acc, const int* __restrict__ cu, int S,
+                                                         int T, int Hq) {
+  pdl_launch_dependents();
+  const int t0 = max(0, cu[0]), t1 = min(T, cu[S]);
+  const long long warp_g = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+  const int lane = threadIdx.x & 31;
+  const long long nwarps = (static_cast<long long>(gridDim.x) * blockDim.x) >> 5;
+  for (long long e = warp_g; e < static_cast<long long>(T) * Hq; e += nwarps) {
+    const int t = static_cast<int>(e / Hq), h = static_cast<int>(e % Hq);  // heads of a token are neighbours in memory
+    if (t < t0 || t >= t1) continue;
+    const long long row = static_cast<long long>(h) * T + t;
+    auto piece = [&](const Rows& x) {
+      return reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(x.p) + t * x.ts + h * x.hs)[lane];
+    };
+    float acc = 0.f;
+    if (lane * 8 < D) {
+      const uint4 a4 = piece(o);
+      const uint4 b4 = piece(dout);
+      const uint4 r4 = resid.p ? piece(resid) : make_uint4(0, 0, 0, 0);
+      const __nv_bfloat162* a2 = reinterpret_cast<const __nv_bfloat162*>(&a4);
+      const __nv_bfloat162* b2 = reinterpret_cast<const __nv_bfloat162*>(&b4);
+      const __nv_bfloat162* r2 = reinterpret_cast<const __nv_bfloat162*>(&r4);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 fa = __bfloat1622float2(a2[k]);
+        const float2 fr = __bfloat1622float2(r2[k]);
+        const float2 fb = __bfloat1622float2(b2[k]);
+        acc = fmaf(fa.x + fr.x, fb.x, acc);
+        acc = fmaf(fa.y + fr.y, fb.y, acc);
+      }
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
+    if (lane == 0) dsum[row] = acc;
+    float4* z = reinterpret_cast<float4*>(dq_acc + row * D);
+    for (int k = lane; k < D / 4; k += 32) z[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+}
+
+// dq = bf16(scale * accumulator) for the packed rows, 8 elements per thread
+// and step; nothing when the plan found the offsets out of range.
+__global__ void __launch_bounds__(256) packed_post_kernel(const float* __restrict__ dq_acc, Rows dq, float scale,
+                                                          const PlanHeader* head, const int* __restrict__ cu, int S,
+                                                          int T, int Hq, int D) {
+  if (head->items == 0) return;
+  const int t0 = max(0, cu[0]), t1 = min(T, cu[S]);
+  const int pieces = D / 8;
+  const long long n = static_cast<long long>(t1 - t0) * Hq * pieces;
+  const long long stride = static_cast<long long>(gridDim.x) * blockDim.x;
+  for (long long e = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; e < n; e += stride) {
+    const long long th = e / pieces;
+    const int c = static_cast<int>(e - th * pieces);
+    const long long t = t0 + th / Hq;
+    const int h = static_cast<int>(th % Hq);
+    const float4* src = reinterpret_cast<const float4*>(dq_acc + (static_cast<long long>(h) * T + t) * D + c * 8);
+    const float4 x = src[0], y = src[1];
+    uint4 out;
+    out.x = pack_bf16x2(x.x * scale, x.y * scale);
+    out.y = pack_bf16x2(x.z * scale, x.w * scale);
+    out.z = pack_bf16x2(y.x * scale, y.y * scale);
+    out.w = pack_bf16x2(y.z * scale, y.w * scale);
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(dq.p) + t * dq.ts + h * dq.hs + c * 8) = out;
+  }
+}
+
+struct PackedBwdLayout {
+  PlanLayout plan;
+  long long max_items;
+  size_t off_d, off_dq, bytes;
+};
+
+PackedBwdLayout packed_bwd_layout(const SeqShape& s) {
+  PackedBwdLayout x;
+  x.max_items = plan_max_units(s.S, s.T, kKT);
+  x.plan = plan_layout(s.S, x.max_items, 0);
+  auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+  x.off_d = up(x.plan.bytes);
+  const size_t rows = static_cast<size_t>(s.T) * s.Hq;
+  x.off_dq = up(x.off_d + rows * 4);
+  x.bytes = x.off_dq + rows * s.d * 4;
+  return x;
+}
+
+template <int D, int MASK>
+cudaError_t launch_packed_bwd_t(const SeqShape& s, const PackedBwdLayout& x, const CUtensorMap& tq,
+                                const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tdo,
+                                const CUtensorMap& tdk, const CUtensorMap& tdv, const Rows& o, const Rows& resid,
+                                const Rows& dout, const float* lse, const Rows& dq, const Rows& dk, const Rows& dv,
+                                void* workspace, const LaunchCtl& ctl, cudaStream_t stream) {
+  using C = BwdCfg<D>;
+  auto kern = bwd_main_kernel<D, MASK, true>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  float* dsum = reinterpret_cast<float*>(ws + x.off_d);
+  float* dq_acc = reinterpret_cast<float*>(ws + x.off_dq);
+  PlanArgs p{};
+  p.cu = s.cu;
+  p.S = s.S;
+  p.T = s.T;
+  p.max_q = s.T;
+  p.max_len = s.T;
+  p.unit = kKT;
+  p.causal = s.causal;
+  p.backward = 1;
+  p.heads = s.Hkv;
+  p.upre = reinterpret_cast<int*>(ws + x.plan.upre);
+  p.head = reinterpret_cast<PlanHeader*>(ws + x.plan.head);
+  p.items = reinterpret_cast<PlanItem*>(ws + x.plan.items);
+  p.slots = reinterpret_cast<int*>(ws + x.plan.slots);
+  p.err = ctl.err;
+  plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  const long long rows = static_cast<long long>(s.T) * s.Hq;
+  packed_pre_kernel<D><<<grid_for(rows, 8, 148 * 64), 256, 0, stream>>>(o, resid, dout, dsum, dq_acc, s.cu, s.S, s.T,
+                                                                       s.Hq);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  BwdArgs a{};
+  a.lse = lse;
+  a.dsum = dsum;
+  a.dq_acc = dq_acc;
+  a.N = s.T;
+  a.Hq = s.Hq;
+  a.Hkv = s.Hkv;
+  a.BHkv = s.Hkv;
+  a.scale = s.scale;
+  a.scale_log2 = s.scale * kLog2e;
+  a.head = p.head;
+  a.items = p.items;
+  a.cu = s.cu;
+  a.dk = dk;
+  a.dv = dv;
+  a.ctl = ctl;
+  const long long grid = x.max_items * s.Hkv;
+  if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  kern<<<static_cast<unsigned>(grid), kThreads, C::kSmemBytes, stream>>>(tq, tk, tv, tdo, tdk, tdv, a);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  packed_post_kernel<<<grid_for(rows * D / 8, 256, 148 * 32), 256, 0, stream>>>(dq_acc, dq, s.scale, p.head, s.cu, s.S,
+                                                                               s.T, s.Hq, D);
+  return cudaGetLastError();
+}
+
 }  // namespace
+
+size_t packed_bwd_workspace_bytes(const SeqShape& s) { return packed_bwd_layout(s).bytes; }
+
+cudaError_t launch_packed_bwd(const SeqShape& s, const Rows& q, const Rows& k, const Rows& v, const Rows& o,
+                              const Rows& resid, const Rows& dout, const float* lse, const Rows& dq, const Rows& dk,
+                              const Rows& dv, void* workspace, const LaunchCtl& ctl, cudaStream_t stream) {
+  const PackedBwdLayout x = packed_bwd_layout(s);
+  CUtensorMap tq, tk, tv, tdo, tdk, tdv;
+  if (!encode_rows_map(&tq, q, s.T, s.Hq, s.d, kQT) || !encode_rows_map(&tk, k, s.T, s.Hkv, s.d, kKT) ||
+      !encode_rows_map(&tv, v, s.T, s.Hkv, s.d, kKT) || !encode_rows_map(&tdo, dout, s.T, s.Hq, s.d, kQT) ||
+      !encode_rows_map(&tdk, dk, s.T, s.Hkv, s.d, kKT) || !encode_rows_map(&tdv, dv, s.T, s.Hkv, s.d, kKT))
+    return cudaErrorInvalidValue;
+#define FA_ARGS s, x, tq, tk, tv, tdo, tdk, tdv, o, resid, dout, lse, dq, dk, dv, workspace, ctl, stream
+  if (s.d == 64) return s.causal ? launch_packed_bwd_t<64, 1>(FA_ARGS) : launch_packed_bwd_t<64, 0>(FA_ARGS);
+  return s.causal ? launch_packed_bwd_t<128, 1>(FA_ARGS) : launch_packed_bwd_t<128, 0>(FA_ARGS);
+#undef FA_ARGS
+}
 
 size_t bwd_workspace_bytes(const AttnShape& s) {
   const size_t rows = static_cast<size_t>(s.B) * s.Hq * s.N;

@@ -121,4 +121,122 @@ cudaError_t launch_decode(const DecodeShape& s, const DecodePlan& plan, const CU
                           const CUtensorMap& tk, const CUtensorMap& tv, void* o, float* lse, void* workspace,
                           const LaunchCtl& ctl, cudaStream_t stream);
 
+// ------------------------------------------ packed sequences, paged cache
+
+// Device views with strides in elements and contiguous rows of d elements:
+// [tokens][heads][d] and [pages][heads][slots][d].
+struct Rows {
+  void* p;
+  long long ts, hs;  // token and head stride
+};
+struct Pages {
+  void* p;
+  long long ps, hs, ss;  // page, head and slot stride
+};
+
+// Encodes a bf16 tensor map of `rank` dimensions (innermost first, strides
+// in bytes of dimensions 1..rank-1) with a box of 64 columns and 128-byte
+// swizzle. Returns false on failure.
+bool encode_bf16_map(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+                     const uint32_t* box);
+
+// Sequence layout of a packed call: sequence b holds tokens [cu[b], cu[b+1])
+// of the T rows. cu == nullptr: one token each (S == T).
+struct SeqShape {
+  int S, T;
+  const int* cu;
+  int Hq, Hkv, d;
+  int causal;
+  float scale;
+  int r() const { return Hq / Hkv; }
+};
+
+// Paged cache: sequence b's keys are the first lens[b] slots of the pages
+// table[b * table_stride + 0, 1, ...].
+struct CacheShape {
+  int n_pages, page, max_pages;
+  const int* lens;
+  const int* table;
+  long long table_stride;
+  int max_q;  // no sequence of the call has more new tokens
+};
+
+// Rows per TMA box of a page: the largest power of two that divides both a
+// page and a 128-key tile, so that no box straddles pages.
+inline int page_box(int page) {
+  int b = 1;
+  while (b < 128 && page % (2 * b) == 0) b *= 2;
+  return b;
+}
+
+// True when every sequence's query rows of a KV head fit one 128-row tile:
+// these calls take the few-row kernel (fa_paged.cu), the others the prompt
+// kernel (fa_packed.cu).
+inline bool paged_few_rows(const SeqShape& s, const CacheShape& c) {
+  return static_cast<long long>(s.r()) * c.max_q <= 128;
+}
+
+size_t paged_few_workspace_bytes(const SeqShape& s, const CacheShape& c, int ctas);
+cudaError_t launch_paged_few(const SeqShape& s, const CacheShape& c, const Rows& q, const Rows& o, const Pages& k,
+                             const Pages& v, float* lse, void* workspace, int sms, const LaunchCtl& ctl,
+                             cudaStream_t stream);
+
+// Work list of the prompt kernels (forward: items of query tokens; backward:
+// key tiles), written by a one-block kernel into the workspace.
+struct PlanItem {
+  int seq, tok0, j0, j1;  // sequence, first token, key tiles [j0, j1) (backward: key tile j0)
+};
+
+size_t packed_fwd_workspace_bytes(const SeqShape& s, const CacheShape* c, int ctas);
+cudaError_t launch_packed_fwd(const SeqShape& s, const CacheShape* c, const Rows& q, const Rows& o, const Rows& resid,
+                              const Rows& krows, const Rows& vrows, const Pages& kpages, const Pages& vpages,
+                              float* lse, void* workspace, int sms, const LaunchCtl& ctl, cudaStream_t stream);
+
+size_t packed_bwd_workspace_bytes(const SeqShape& s);
+cudaError_t launch_packed_bwd(const SeqShape& s, const Rows& q, const Rows& k, const Rows& v, const Rows& o,
+                              const Rows& resid, const Rows& dout, const float* lse, const Rows& dq, const Rows& dk,
+                              const Rows& dv, void* workspace, const LaunchCtl& ctl, cudaStream_t stream);
+
+// 3-D map of a [T][H][d] view, box_rows tokens of one head; and the 4-D map
+// (d, heads of a KV group, tokens, KV heads) whose box is all r heads of a
+// group times `tokens` tokens, in token-major order.
+bool encode_rows_map(CUtensorMap* map, const Rows& x, int T, int H, int d, int box_rows);
+bool encode_group_map(CUtensorMap* map, const Rows& x, int T, int Hkv, int r, int d, int tokens);
+// 4-D map (d, slots, heads, pages) of a paged tensor, box_rows slots of one head.
+bool encode_pages_map(CUtensorMap* map, const Pages& x, int n_pages, int Hkv, int page, int d, int box_rows);
+
+// Sequence b's tokens [start, start + n), or n = 0 when its offsets or
+// length are out of range. `lens`/`max_len` only for a paged cache.
+struct SeqRange {
+  int start, n, len;
+  bool bad;
+};
+__host__ __device__ inline SeqRange seq_range(const int* cu, const int* lens, int b, int T, int max_q, long long max_len) {
+  SeqRange x;
+  x.start = cu ? cu[b] : b;
+  const long long end = cu ? cu[b + 1] : static_cast<long long>(b) + 1;
+  const long long n = end - x.start;
+  x.len = lens ? lens[b] : static_cast<int>(n < 0 ? 0 : n);
+  x.bad = x.start < 0 || n < 0 || end > T || n > max_q || x.len < 0 || x.len > max_len;
+  x.n = x.bad ? 0 : static_cast<int>(n);
+  return x;
+}
+
+// Rotary positions and the append to a paged cache (fa_rope.cu).
+struct RopeShape {
+  int T, Hq, Hkv, d;
+  int pairs;          // rotated pairs (0: no rotation)
+  int interleaved;    // pairs (2i, 2i + 1), else (i, i + pairs)
+  float sign;         // -1: the inverse rotation
+  const int* positions;  // [axes][T]
+  const double* inv_freq;  // [pairs], radians per position
+  int n_sections;
+  int section_end[4];  // pair i goes by axis a for section_end[a-1] <= i < section_end[a]
+};
+cudaError_t launch_rope(const RopeShape& s, const Rows& q, const Rows& k, const Rows& q_out, const Rows& k_out,
+                        cudaStream_t stream);
+cudaError_t launch_paged_append(const RopeShape& s, const SeqShape& seq, const CacheShape& c, const Rows& q,
+                                const Rows& k, const Rows& v, const Rows& q_out, const Pages& k_pages,
+                                const Pages& v_pages, unsigned int* err, cudaStream_t stream);
+
 }  // namespace fa

@@ -96,7 +96,10 @@ struct Watch {
   uint64_t budget_ns;        // per-wait budget
 };
 
-enum : unsigned int { kErrTimeout = 1u };
+// Bits of the device error word: a bounded wait ran out; a kernel found no
+// room to align its shared memory; lengths, offsets or page numbers in device
+// memory are out of range.
+enum : unsigned int { kErrTimeout = 1u, kErrAlign = 2u, kErrData = 4u };
 
 // Wait until the phase of parity `parity` of `bar` has completed. Returns
 // false (without waiting further) once the CTA is aborting or the budget is
@@ -149,6 +152,16 @@ __device__ __forceinline__ void tma_load_3d(const CUtensorMap* m, uint64_t* bar,
       : "memory");
 }
 
+// 4-D tiled load, otherwise as tma_load_3d.
+__device__ __forceinline__ void tma_load_4d(const CUtensorMap* m, uint64_t* bar, void* dst, int c0, int c1, int c2,
+                                            int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(m), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+
 // 3-D tiled store of a shared-memory box (in the tensor map's swizzled
 // layout) to global memory; elements outside the tensor are not written.
 // Completes as a bulk async-group (bulk_commit / bulk_wait_read). No
@@ -156,6 +169,12 @@ __device__ __forceinline__ void tma_load_3d(const CUtensorMap* m, uint64_t* bar,
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* m, const void* src, int c0, int c1, int c2) {
   asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(m),
                "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
+// 4-D tiled store, otherwise as tma_store_3d.
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap* m, const void* src, int c0, int c1, int c2, int c3) {
+  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(m),
+               "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
                : "memory");
 }
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
@@ -169,6 +188,11 @@ __device__ __forceinline__ void bulk_wait_read() {
 __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
+// Programmatic dependent launch: lets the dependent grid be scheduled, and
+// waits until the grids this one depends on have finished and their writes
+// are visible (both return at once in a grid launched without the attribute).
+__device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // Barrier `id` (1..15) over `n` threads (a multiple of 32).
 __device__ __forceinline__ void named_bar_sync(int id, int n) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");

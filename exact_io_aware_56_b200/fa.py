@@ -21,6 +21,7 @@ FA_ERR_INVALID_ARGUMENT = 1
 FA_ERR_UNSUPPORTED = 2
 FA_ERR_CUDA = 3
 FA_ERR_TIMEOUT = 4
+FA_ERR_DATA = 5
 
 _lib = None
 
@@ -29,6 +30,19 @@ class FaError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
         super().__init__(f"{where}: status {status}: {status_string(status)}")
+
+
+class Rows(ctypes.Structure):
+    """``fa_rows``: a [T][H][d] view, strides in elements."""
+
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class Pages(ctypes.Structure):
+    """``fa_pages``: a [n_pages][Hkv][page_size][d] view, strides in elements."""
+
+    _fields_ = [("data", ctypes.c_void_p), ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("slot_stride", ctypes.c_int64)]
 
 
 def lib() -> ctypes.CDLL:
@@ -62,6 +76,24 @@ def lib() -> ctypes.CDLL:
     L.fa_decode_workspace_bytes.restype = sz
     L.fa_decode.argtypes = [vp] * 5 + [i, i, i, i, i, i, i, f, vp, sz, vp]
     L.fa_decode.restype = i
+    rows, pages, i64 = ctypes.POINTER(Rows), ctypes.POINTER(Pages), ctypes.c_int64
+    L.fa_packed_fwd_workspace_bytes.argtypes = [i] * 5
+    L.fa_packed_fwd_workspace_bytes.restype = sz
+    L.fa_packed_fwd.argtypes = [rows] * 5 + [vp, vp] + [i] * 6 + [f, vp, sz, vp]
+    L.fa_packed_fwd.restype = i
+    L.fa_packed_bwd_workspace_bytes.argtypes = [i] * 5
+    L.fa_packed_bwd_workspace_bytes.restype = sz
+    L.fa_packed_bwd.argtypes = [rows] * 6 + [vp] + [rows] * 3 + [vp] + [i] * 6 + [f, vp, sz, vp]
+    L.fa_packed_bwd.restype = i
+    L.fa_paged_fwd_workspace_bytes.argtypes = [i] * 8
+    L.fa_paged_fwd_workspace_bytes.restype = sz
+    L.fa_paged_fwd.argtypes = [rows, pages, pages, rows, vp, i, i, vp, i64, i, vp, vp] + [i] * 7 + [f, vp, sz, vp]
+    L.fa_paged_fwd.restype = i
+    L.fa_paged_append.argtypes = ([rows] * 4 + [pages] * 2 + [i, i, vp, i64, i, vp, vp, i, i, vp, vp, vp] + [i] * 5 +
+                                  [vp])
+    L.fa_paged_append.restype = i
+    L.fa_rope.argtypes = [rows] * 4 + [vp, vp, vp] + [i] * 7 + [vp]
+    L.fa_rope.restype = i
     L.fa_status_string.argtypes = [i]
     L.fa_status_string.restype = ctypes.c_char_p
     L.fa_check_device_error.argtypes = [vp]
@@ -247,6 +279,212 @@ def fa_decode(q, k, v, o, lse, causal: bool, scale: float, workspace, stream=Non
         raise FaError(rc, "fa_decode")
 
 
+# ------------------------------------------ packed sequences, paged cache
+
+def _check_view(name, t, dtype, shape, dev):
+    """A CUDA tensor of this type and shape on device ``dev`` whose last dimension is contiguous; its strides."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise RuntimeError(f"{name} must be a CUDA tensor (there is no CPU path)")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()} but the current device is cuda:{dev}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] > 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    return st
+
+
+def _rows(name, t, shape, dev):
+    st = _check_view(name, t, torch.bfloat16, shape, dev)
+    return Rows(t.data_ptr(), st[0], st[1])
+
+
+def _pages(name, t, shape, dev):
+    st = _check_view(name, t, torch.bfloat16, shape, dev)
+    return Pages(t.data_ptr(), st[0], st[1], st[2])
+
+
+def _flat(name, t, dtype, shape, dev):
+    """Address of a contiguous tensor (``None`` for ``None``)."""
+    if t is None:
+        return None
+    _check_view(name, t, dtype, shape, dev)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _workspace(t, dev):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or not t.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"workspace is on cuda:{t.get_device()} but the current device is cuda:{dev}")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _three(name, t):
+    if not isinstance(t, torch.Tensor) or t.dim() != 3:
+        raise ValueError(f"{name} must be a [T, H, d] tensor")
+    return t.shape
+
+
+def _seqs(cu_seqlens, T, dev):
+    """(S, address) of the offsets; ``None``: one token per sequence."""
+    if cu_seqlens is None:
+        return T, None
+    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must be a tensor of S + 1 offsets")
+    return cu_seqlens.numel() - 1, _flat("cu_seqlens", cu_seqlens, torch.int32, cu_seqlens.shape, dev)
+
+
+def _ok(rc, where):
+    if rc != FA_OK:
+        raise FaError(rc, where)
+
+
+def fa_packed_fwd_workspace_bytes(S: int, T: int, Hq: int, Hkv: int, d: int) -> int:
+    return int(lib().fa_packed_fwd_workspace_bytes(S, T, Hq, Hkv, d))
+
+
+def fa_packed_fwd(q, k, v, o, lse, cu_seqlens, causal: bool, scale: float, workspace, stream=None,
+                  o_resid=None) -> None:
+    """Forward over packed sequences: ``q``, ``o`` (and ``o_resid``) [T,Hq,d], ``k``, ``v`` [T,Hkv,d] bf16 views,
+    ``lse`` [Hq,T] fp32, ``cu_seqlens`` int32 [S+1]; ``workspace`` a uint8 CUDA tensor of at least
+    :func:`fa_packed_fwd_workspace_bytes` bytes."""
+    dev = torch.cuda.current_device()
+    sq, sk = _three("q", q), _three("k", k)
+    T, Hq, d = sq
+    sk = torch.Size((T, sk[1], d))
+    S, cu = _seqs(cu_seqlens, T, dev)
+    if cu is None:
+        raise ValueError("cu_seqlens is required")
+    args = [_rows("q", q, sq, dev), _rows("k", k, sk, dev), _rows("v", v, sk, dev), _rows("o", o, sq, dev),
+            None if o_resid is None else _rows("o_resid", o_resid, sq, dev)]
+    la = _flat("lse", lse, torch.float32, (Hq, T), dev)
+    wa, wb = _workspace(workspace, dev)
+    _ok(lib().fa_packed_fwd(*args, la, cu, S, T, Hq, sk[1], d, int(bool(causal)), float(scale), wa, wb,
+                            _stream(stream)), "fa_packed_fwd")
+
+
+def fa_packed_bwd_workspace_bytes(S: int, T: int, Hq: int, Hkv: int, d: int) -> int:
+    return int(lib().fa_packed_bwd_workspace_bytes(S, T, Hq, Hkv, d))
+
+
+def fa_packed_bwd(q, k, v, o, dout, lse, dq, dk, dv, cu_seqlens, causal: bool, scale: float, workspace, stream=None,
+                  o_resid=None) -> None:
+    """Backward of :func:`fa_packed_fwd` into ``dq`` [T,Hq,d], ``dk``, ``dv`` [T,Hkv,d]."""
+    dev = torch.cuda.current_device()
+    sq, sk = _three("q", q), _three("k", k)
+    T, Hq, d = sq
+    sk = torch.Size((T, sk[1], d))
+    S, cu = _seqs(cu_seqlens, T, dev)
+    if cu is None:
+        raise ValueError("cu_seqlens is required")
+    ins = [_rows("q", q, sq, dev), _rows("k", k, sk, dev), _rows("v", v, sk, dev), _rows("o", o, sq, dev),
+           None if o_resid is None else _rows("o_resid", o_resid, sq, dev), _rows("dout", dout, sq, dev)]
+    la = _flat("lse", lse, torch.float32, (Hq, T), dev)
+    outs = [_rows("dq", dq, sq, dev), _rows("dk", dk, sk, dev), _rows("dv", dv, sk, dev)]
+    wa, wb = _workspace(workspace, dev)
+    _ok(lib().fa_packed_bwd(*ins, la, *outs, cu, S, T, Hq, sk[1], d, int(bool(causal)), float(scale), wa, wb,
+                            _stream(stream)), "fa_packed_bwd")
+
+
+def _cache(k_pages, v_pages, block_table, seq_lens, S, Hkv, d, dev):
+    if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
+        raise ValueError("k_pages must be [n_pages, Hkv, page_size, d]")
+    shape = torch.Size((k_pages.shape[0], Hkv, k_pages.shape[2], d))
+    kp, vp = _pages("k_pages", k_pages, shape, dev), _pages("v_pages", v_pages, shape, dev)
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be [S, max_pages]")
+    bt = _check_view("block_table", block_table, torch.int32, (S, block_table.shape[1]), dev)
+    ln = _flat("seq_lens", seq_lens, torch.int32, (S,), dev)
+    if ln is None:
+        raise ValueError("seq_lens is required")
+    return kp, vp, shape[0], shape[2], block_table.data_ptr(), bt[0], block_table.shape[1], ln
+
+
+def fa_paged_fwd_workspace_bytes(S: int, T: int, max_q: int, Hq: int, Hkv: int, d: int, page_size: int,
+                                 max_pages: int) -> int:
+    return int(lib().fa_paged_fwd_workspace_bytes(S, T, max_q, Hq, Hkv, d, page_size, max_pages))
+
+
+def fa_paged_fwd(q, k_pages, v_pages, o, lse, block_table, seq_lens, cu_seqlens, max_q: int, causal: bool,
+                 scale: float, workspace, stream=None) -> None:
+    """Attention of new tokens ``q`` [T,Hq,d] over a paged cache ``k_pages``, ``v_pages``
+    [n_pages,Hkv,page_size,d] into ``o`` [T,Hq,d] and ``lse`` [Hq,T]; ``block_table`` int32 [S,max_pages],
+    ``seq_lens`` int32 [S] (new tokens counted), ``cu_seqlens`` int32 [S+1] or ``None`` (one token each), no
+    sequence with more than ``max_q`` new tokens."""
+    dev = torch.cuda.current_device()
+    sq = _three("q", q)
+    T, Hq, d = sq
+    S, cu = _seqs(cu_seqlens, T, dev)
+    Hkv = k_pages.shape[1] if isinstance(k_pages, torch.Tensor) and k_pages.dim() == 4 else 0
+    kp, vp, n_pages, page, bt, bts, max_pages, ln = _cache(k_pages, v_pages, block_table, seq_lens, S, Hkv, d, dev)
+    qa, oa = _rows("q", q, sq, dev), _rows("o", o, sq, dev)
+    la = _flat("lse", lse, torch.float32, (Hq, T), dev)
+    wa, wb = _workspace(workspace, dev)
+    _ok(lib().fa_paged_fwd(qa, kp, vp, oa, la, n_pages, page, bt, bts, max_pages, ln, cu, S, T, int(max_q), Hq, Hkv, d,
+                           int(bool(causal)), float(scale), wa, wb, _stream(stream)), "fa_paged_fwd")
+
+
+def _sections(sections, inv_freq):
+    if inv_freq is None:
+        if sections is not None and len(sections):
+            raise ValueError("sections need inv_freq")
+        return 0, None, 0
+    sections = [inv_freq.numel()] if sections is None else [int(n) for n in sections]
+    if sum(sections) != inv_freq.numel():
+        raise ValueError(f"sections {sections} must sum to inv_freq's {inv_freq.numel()} pairs")
+    return len(sections), (ctypes.c_int * len(sections))(*sections), inv_freq.numel()
+
+
+def fa_rope(q, k, q_out, k_out, positions, inv_freq, sections=None, interleaved: bool = False, inverse: bool = False,
+            stream=None) -> None:
+    """Rotary positions of ``q`` [T,Hq,d] and ``k`` [T,Hkv,d] (either may be ``None``) into ``q_out``, ``k_out``
+    (which may be ``q``, ``k``): ``positions`` int32 [axes,T], ``inv_freq`` float64 [pairs], ``sections`` the pairs
+    of each axis (default: all of axis 0)."""
+    dev = torch.cuda.current_device()
+    if q is None and k is None:
+        raise ValueError("q or k is required")
+    T, _, d = _three("q" if q is not None else "k", q if q is not None else k)
+    sq = torch.Size((T, 0, d)) if q is None else _three("q", q)
+    sk = torch.Size((T, 0, d)) if k is None else torch.Size((T, _three("k", k)[1], d))
+    if inv_freq is None or positions is None:
+        raise ValueError("positions and inv_freq are required")
+    n, sec, pairs = _sections(sections, inv_freq)
+    fa_ = _flat("inv_freq", inv_freq, torch.float64, (pairs,), dev)
+    pa = _flat("positions", positions, torch.int32, (n, T), dev)
+    args = [None if q is None else _rows("q", q, sq, dev), None if k is None else _rows("k", k, sk, dev),
+            None if q is None else _rows("q_out", q_out, sq, dev), None if k is None else _rows("k_out", k_out, sk, dev)]
+    _ok(lib().fa_rope(*args, pa, fa_, sec, n, T, sq[1], sk[1], d, int(bool(interleaved)), int(bool(inverse)),
+                      _stream(stream)), "fa_rope")
+
+
+def fa_paged_append(q, k, v, q_out, k_pages, v_pages, block_table, seq_lens, cu_seqlens, positions=None, inv_freq=None,
+                    sections=None, interleaved: bool = False, stream=None) -> None:
+    """Appends ``k``, ``v`` [T,Hkv,d] of the new tokens to the paged cache, in place; with ``inv_freq`` the keys are
+    turned first, and ``q`` [T,Hq,d] (or ``None``) into ``q_out``, by ``positions`` int32 [axes,T] (``None``: the
+    places in the cache). Cache arguments as :func:`fa_paged_fwd`."""
+    dev = torch.cuda.current_device()
+    sk = _three("k", k)
+    T, Hkv, d = sk
+    sq = torch.Size((T, 0, d)) if q is None else torch.Size((T, _three("q", q)[1], d))
+    S, cu = _seqs(cu_seqlens, T, dev)
+    kp, vp, n_pages, page, bt, bts, max_pages, ln = _cache(k_pages, v_pages, block_table, seq_lens, S, Hkv, d, dev)
+    n, sec, pairs = _sections(sections, inv_freq)
+    fa_ = _flat("inv_freq", inv_freq, torch.float64, (pairs,), dev)
+    pa = _flat("positions", positions, torch.int32, (n, T), dev)
+    args = [None if q is None else _rows("q", q, sq, dev), _rows("k", k, sk, dev), _rows("v", v, sk, dev),
+            None if q is None else _rows("q_out", q_out, sq, dev)]
+    _ok(lib().fa_paged_append(*args, kp, vp, n_pages, page, bt, bts, max_pages, ln, cu, S, T, pa, fa_, sec, n, sq[1],
+                              Hkv, d, int(bool(interleaved)), _stream(stream)), "fa_paged_append")
+
+
 def fa_check_device_error(stream=None) -> int:
     return int(lib().fa_check_device_error(_stream(stream)))
 
@@ -341,3 +579,103 @@ def attention_forward_fp8(q, k, v, causal: bool, scale: float | None = None, str
     lse = torch.empty((B, Hq, N), dtype=torch.float32, device=q.device)
     fa_fwd_fp8(q8, sq, k8, sk, v8, sv, o, lse, causal, scale, stream)
     return o, lse, (q8, sq, k8, sk, v8, sv)
+
+
+class _Allocate:
+    """Memory for one call on ``stream``: new tensors belong to that stream, and the caching allocator learns that
+    the call's inputs are used on it."""
+
+    def __init__(self, stream, *inputs):
+        self.stream = None
+        if stream is not None:
+            s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream))
+            if s != torch.cuda.current_stream():
+                self.stream = s
+                for t in inputs:
+                    if isinstance(t, torch.Tensor) and t.is_cuda:
+                        t.record_stream(s)
+
+    def empty(self, shape, dtype, device):
+        if self.stream is None:
+            return torch.empty(shape, dtype=dtype, device=device)
+        with torch.cuda.stream(self.stream):
+            return torch.empty(shape, dtype=dtype, device=device)
+
+    def bytes(self, n, device):
+        return self.empty(max(16, n), torch.uint8, device)
+
+
+def attention_packed_forward(q, k, v, cu_seqlens, causal: bool, scale: float | None = None, stream=None,
+                             residual: bool = False, workspace=None):
+    """Allocates the outputs (and the workspace if not given) and runs :func:`fa_packed_fwd`.
+
+    Returns ``(o, lse)``, or ``(o, lse, o_resid)`` when ``residual`` is true. Rows outside every sequence are not
+    written.
+    """
+    T, Hq, d = _three("q", q)
+    scale = d ** -0.5 if scale is None else scale
+    new = _Allocate(stream, q, k, v, cu_seqlens, workspace)
+    if workspace is None:
+        workspace = new.bytes(fa_packed_fwd_workspace_bytes(cu_seqlens.numel() - 1, T, Hq, k.shape[1], d), q.device)
+    o = new.empty((T, Hq, d), q.dtype, q.device)
+    lse = new.empty((Hq, T), torch.float32, q.device)
+    o_resid = new.empty((T, Hq, d), q.dtype, q.device) if residual else None
+    fa_packed_fwd(q, k, v, o, lse, cu_seqlens, causal, scale, workspace, stream, o_resid=o_resid)
+    return (o, lse, o_resid) if residual else (o, lse)
+
+
+def attention_packed_backward(q, k, v, o, dout, lse, cu_seqlens, causal: bool, scale: float | None = None,
+                              workspace=None, stream=None, o_resid=None):
+    """Allocates ``dq``, ``dk``, ``dv`` (and the workspace if not given) and runs :func:`fa_packed_bwd`."""
+    T, Hq, d = _three("q", q)
+    Hkv = _three("k", k)[1]
+    scale = d ** -0.5 if scale is None else scale
+    new = _Allocate(stream, q, k, v, o, dout, lse, cu_seqlens, o_resid, workspace)
+    if workspace is None:
+        workspace = new.bytes(fa_packed_bwd_workspace_bytes(cu_seqlens.numel() - 1, T, Hq, Hkv, d), q.device)
+    dq = new.empty((T, Hq, d), q.dtype, q.device)
+    dk = new.empty((T, Hkv, d), q.dtype, q.device)
+    dv = new.empty((T, Hkv, d), q.dtype, q.device)
+    fa_packed_bwd(q, k, v, o, dout, lse, dq, dk, dv, cu_seqlens, causal, scale, workspace, stream, o_resid=o_resid)
+    return dq, dk, dv
+
+
+def attention_paged(q, k_pages, v_pages, block_table, seq_lens, cu_seqlens=None, max_q: int | None = None,
+                    causal: bool = True, scale: float | None = None, workspace=None, stream=None):
+    """Allocates ``o``, ``lse`` (and the workspace if not given) and runs :func:`fa_paged_fwd`.
+
+    ``cu_seqlens`` ``None``: one new token per sequence. ``max_q`` defaults to 1 then, and otherwise to T (a tight
+    bound picks the faster kernel and needs less workspace). Returns ``(o, lse)``.
+    """
+    T, Hq, d = _three("q", q)
+    scale = d ** -0.5 if scale is None else scale
+    if max_q is None:
+        max_q = 1 if cu_seqlens is None else max(1, T)
+    new = _Allocate(stream, q, k_pages, v_pages, block_table, seq_lens, cu_seqlens, workspace)
+    if workspace is None:
+        S = T if cu_seqlens is None else cu_seqlens.numel() - 1
+        workspace = new.bytes(fa_paged_fwd_workspace_bytes(S, T, max_q, Hq, k_pages.shape[1], d, k_pages.shape[2],
+                                                           block_table.shape[1]), q.device)
+    o = new.empty((T, Hq, d), q.dtype, q.device)
+    lse = new.empty((Hq, T), torch.float32, q.device)
+    fa_paged_fwd(q, k_pages, v_pages, o, lse, block_table, seq_lens, cu_seqlens, max_q, causal, scale, workspace, stream)
+    return o, lse
+
+
+def paged_append(k, v, k_pages, v_pages, block_table, seq_lens, cu_seqlens=None, q=None, positions=None, inv_freq=None,
+                 sections=None, interleaved: bool = False, stream=None):
+    """Runs :func:`fa_paged_append`; returns the (turned) ``q`` in a new tensor, or ``None`` without ``q``."""
+    new = _Allocate(stream, q, k, v, k_pages, v_pages, block_table, seq_lens, cu_seqlens, positions, inv_freq)
+    q_out = None if q is None else new.empty(_three("q", q), q.dtype, q.device)
+    fa_paged_append(q, k, v, q_out, k_pages, v_pages, block_table, seq_lens, cu_seqlens, positions, inv_freq, sections,
+                    interleaved, stream)
+    return q_out
+
+
+def rope(q, k, positions, inv_freq, sections=None, interleaved: bool = False, inverse: bool = False, stream=None):
+    """Allocates the outputs and runs :func:`fa_rope`; returns ``(q_out, k_out)`` (``None`` for ``None``)."""
+    new = _Allocate(stream, q, k, positions, inv_freq)
+    q_out = None if q is None else new.empty(_three("q", q), q.dtype, q.device)
+    k_out = None if k is None else new.empty(_three("k", k), k.dtype, k.device)
+    fa_rope(q, k, q_out, k_out, positions, inv_freq, sections, interleaved, inverse, stream)
+    return q_out, k_out

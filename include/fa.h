@@ -55,6 +55,7 @@ extern "C" {
 #define FA_ERR_UNSUPPORTED 2
 #define FA_ERR_CUDA 3
 #define FA_ERR_TIMEOUT 4
+#define FA_ERR_DATA 5
 
 /*
  * Forward pass: o = softmax(scale * q k^T [causal]) v and lse = row
@@ -268,6 +269,139 @@ size_t fa_decode_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int d);
 int fa_decode(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq, int Hkv, int Nq,
               int Nk, int d, int causal, float scale, void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * Packed sequences and the paged cache.
+ *
+ * Sequences of different lengths lie one after another in a packed tensor of
+ * T tokens: sequence b is tokens [cu_seqlens[b], cu_seqlens[b + 1]), S + 1
+ * non-decreasing int32 in device memory, cu_seqlens[0] >= 0,
+ * cu_seqlens[S] <= T. Sequences may be empty. Tokens outside all of them are
+ * not read into any result, and their outputs are left as they were. The
+ * offsets and lengths are read on the device, so that a captured call can be
+ * replayed on other ones (same T, S and, paged, max_q).
+ *
+ * fa_rows is a [T][H][d] bf16 view and fa_pages a [n_pages][Hkv][page_size][d]
+ * bf16 view; d is contiguous, the other strides are in elements, positive
+ * multiples of 8 (any value along an axis of one element), data 16-byte
+ * aligned. A slice of a fused projection or a transposed [H][T][d] tensor is
+ * such a view. Outputs must not overlap inputs or one another, except where
+ * said.
+ *
+ * Supported: d in {64, 128}; Hq a multiple of Hkv, Hq / Hkv <= 128; page_size
+ * a multiple of 8; max_pages * page_size <= 2^30. S = 0 or T = 0 returns
+ * FA_OK and does nothing.
+ *
+ * Offsets out of order or range, lengths out of range and page numbers
+ * outside the pool are found on the device: kernels never access memory
+ * outside the tensors for them, and fa_check_device_error returns FA_ERR_DATA
+ * (or FA_ERR_TIMEOUT if a wait also ran out). An attention call computes
+ * nothing when an offset or a length is out of range; a page number outside
+ * the pool is read as a page of zeros, and nothing is appended to it.
+ */
+typedef struct fa_rows {
+  void* data;
+  int64_t token_stride;
+  int64_t head_stride;
+} fa_rows;
+
+typedef struct fa_pages {
+  void* data;
+  int64_t page_stride;
+  int64_t head_stride;
+  int64_t slot_stride;
+} fa_pages;
+
+/*
+ * Forward attention over packed sequences: every token attends to its own
+ * sequence, causal = 1 to the tokens not behind it.
+ *   q, o [T][Hq][d], k, v [T][Hkv][d]
+ *   o_resid: NULL, or [T][Hq][d], the rounding residual of o (written), as
+ *     fa_fwd_with_residual; rounding follows fa_fwd without it and
+ *     fa_fwd_with_residual with it.
+ *   lse [Hq][T] fp32, contiguous: row logsumexp (natural log)
+ *   workspace: at least fa_packed_fwd_workspace_bytes(...) bytes, 16-byte
+ *     aligned, contents need not be initialised. Calls that may overlap on
+ *     the GPU (other streams, captured graphs) need workspaces of their own.
+ */
+size_t fa_packed_fwd_workspace_bytes(int S, int T, int Hq, int Hkv, int d);
+int fa_packed_fwd(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa_rows* o, const fa_rows* o_resid,
+                  float* lse, const int* cu_seqlens, int S, int T, int Hq, int Hkv, int d, int causal, float scale,
+                  void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradients of sum(dout * o) for fa_packed_fwd, rebuilding P from q, k and
+ * lse as fa_bwd does; o_resid (NULL or as written by the forward) sharpens
+ * D_i as in fa_bwd_with_residual. dq [T][Hq][d], dk, dv [T][Hkv][d] are
+ * written, not accumulated into. dq is summed over key tiles by fp32 atomic
+ * additions, as in fa_bwd: its last bits may differ from run to run.
+ */
+size_t fa_packed_bwd_workspace_bytes(int S, int T, int Hq, int Hkv, int d);
+int fa_packed_bwd(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa_rows* o, const fa_rows* o_resid,
+                  const fa_rows* dout, const float* lse, const fa_rows* dq, const fa_rows* dk, const fa_rows* dv,
+                  const int* cu_seqlens, int S, int T, int Hq, int Hkv, int d, int causal, float scale,
+                  void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Attention of new tokens over a paged KV cache, from single-token decode to
+ * chunks of a prompt, mixed freely. Sequence b has n_b = cu_seqlens[b + 1] -
+ * cu_seqlens[b] new tokens (cu_seqlens NULL: S = T, one each), which are the
+ * last of its seq_lens[b] cached tokens (append them first, fa_paged_append):
+ * new token i sits at place p = seq_lens[b] - n_b + i and sees keys j <= p
+ * (causal = 1) or all seq_lens[b]. A token that sees no key (place < 0, or an
+ * empty cache) gets o = 0, lse = -inf.
+ *   q, o [T][Hq][d]; lse [Hq][T] fp32
+ *   k_pages, v_pages [n_pages][Hkv][page_size][d]; key j of sequence b is slot
+ *     j % page_size of page block_table[b * table_stride + j / page_size].
+ *     Pages may be shared between sequences. Slots behind a sequence's end
+ *     may hold anything, NaN included.
+ *   block_table int32 [S][max_pages] (rows table_stride apart); entries past
+ *     a sequence's last page are not read.
+ *   seq_lens int32 [S], 0 <= seq_lens[b] <= max_pages * page_size
+ *   max_q: no n_b is larger (checked on the device); up to 128 query rows
+ *     (max_q * Hq / Hkv) take a kernel that streams the cache once through
+ *     all SMs, more the prompt kernel.
+ *   workspace: as fa_packed_fwd, fa_paged_fwd_workspace_bytes(...) bytes.
+ */
+size_t fa_paged_fwd_workspace_bytes(int S, int T, int max_q, int Hq, int Hkv, int d, int page_size, int max_pages);
+int fa_paged_fwd(const fa_rows* q, const fa_pages* k_pages, const fa_pages* v_pages, const fa_rows* o, float* lse,
+                 int n_pages, int page_size, const int* block_table, int64_t table_stride, int max_pages,
+                 const int* seq_lens, const int* cu_seqlens, int S, int T, int max_q, int Hq, int Hkv, int d,
+                 int causal, float scale, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Rotary positions: turns pair i of every head of q and k, i < pairs = the
+ * sum of sections, by the angle positions[a][t] * inv_freq[i], a being the
+ * section that i falls into (sections[0] pairs go by axis 0, the next
+ * sections[1] by axis 1, ...): (x, y) -> (x cos - y sin, y cos + x sin).
+ * Pairs are elements (i, i + pairs), or (2i, 2i + 1) with interleaved = 1;
+ * elements from 2 * pairs on are copied. inverse = 1 turns the other way,
+ * which is also the backward pass (on dq, dk). Angles are formed in float64.
+ *   q, q_out [T][Hq][d], k, k_out [T][Hkv][d]; Hq or Hkv may be 0 (that
+ *     tensor's arguments are ignored). An output may be its own input (same
+ *     data and strides).
+ *   positions int32 [n_sections][T]; inv_freq float64 [pairs], radians per
+ *     position; both device memory. sections: host array, 1 to 4 entries,
+ *     pairs a multiple of 8, 2 * pairs <= d.
+ */
+int fa_rope(const fa_rows* q, const fa_rows* k, const fa_rows* q_out, const fa_rows* k_out, const int* positions,
+            const double* inv_freq, const int* sections, int n_sections, int T, int Hq, int Hkv, int d,
+            int interleaved, int inverse, void* stream);
+
+/*
+ * Appends the new tokens' keys and values to a paged cache (layout as
+ * fa_paged_fwd; seq_lens count them already): token i of sequence b goes to
+ * place seq_lens[b] - n_b + i; places below 0 are not written. With
+ * n_sections > 0 the keys are turned first, and q into q_out, as by fa_rope;
+ * positions NULL (one section only) means the places. With n_sections = 0
+ * keys are copied (and q into q_out). Hq = 0: no q. q_out may be q. Two tokens
+ * of one call that go to the same slot leave either's value.
+ */
+int fa_paged_append(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa_rows* q_out,
+                    const fa_pages* k_pages, const fa_pages* v_pages, int n_pages, int page_size,
+                    const int* block_table, int64_t table_stride, int max_pages, const int* seq_lens,
+                    const int* cu_seqlens, int S, int T, const int* positions, const double* inv_freq,
+                    const int* sections, int n_sections, int Hq, int Hkv, int d, int interleaved, void* stream);
+
 /* Static text for a status code (for FA_ERR_CUDA: the last CUDA error seen by
  * this thread). Never NULL. */
 const char* fa_status_string(int status);
@@ -275,7 +409,8 @@ const char* fa_status_string(int status);
 /*
  * Synchronises `stream`, then reads and clears the current device's error
  * word. Returns FA_OK, FA_ERR_TIMEOUT when a kernel's bounded wait ran out
- * since the last check, or FA_ERR_CUDA when the synchronisation failed.
+ * since the last check, FA_ERR_DATA when a kernel found offsets, lengths or
+ * page numbers out of range, or FA_ERR_CUDA when the synchronisation failed.
  */
 int fa_check_device_error(void* stream);
 

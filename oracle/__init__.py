@@ -43,6 +43,15 @@ from .fp8 import (  # noqa: F401
     e4m3_encode,
     quantize_blocks,
 )
+from .packed import (  # noqa: F401
+    append_ref,
+    packed_bwd_ref,
+    packed_fwd_ref,
+    paged_keys,
+    paged_ref,
+    places,
+    rope_ref,
+)
 from .memory import (  # noqa: F401
     naive_score_bytes,
     flash_state_bytes,

@@ -1,0 +1,249 @@
+"""GPU parity of attention over a paged cache (fa_paged_fwd) against the fp64 oracle: single tokens, drafted tokens,
+chunks and mixtures; page sizes that end inside a key tile; empty caches and rows without keys; NaN in unused slots;
+strided views; out-of-range pages, lengths and offsets; graphs, streams and guard rows."""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from exact_io_aware_56_b200 import fa, to_f64
+
+from .packed import Cache, assert_forward, done, normal, offsets
+
+pytestmark = pytest.mark.gpu
+
+
+def run(new, lens, page, hq, hkv, d, causal=True, seed=1, max_q=None, token_major=False, cu=None):
+    cache = Cache(seed, lens, page, hkv, d, token_major=token_major)
+    cu = offsets(new) if cu is None else np.array(cu, dtype=np.int32)
+    q = normal(seed + 7, int(cu[-1]), hq, d)
+    kp, vp, table, ln = cache.cuda()
+    o, lse = fa.attention_paged(q.cuda(), kp, vp, table, ln, torch.from_numpy(cu).cuda(),
+                                max(new) if max_q is None else max_q, causal, 0.125)
+    done()
+    ref = oracle.paged_ref(to_f64(q), to_f64(cache.k), to_f64(cache.v), cache.table, cache.lens, cu, causal, 0.125)
+    assert_forward(o, lse, *ref)
+    return o, lse
+
+
+# (new tokens, cached tokens, page, Hq, Hkv)
+FEW = [
+    ([1], [1], 16, 1, 1),
+    ([1], [129], 16, 16, 16),
+    ([1, 1, 1], [1000, 1, 257], 64, 8, 2),
+    ([4, 1, 3], [300, 64, 3], 32, 8, 1),        # 32 rows: four copies
+    ([8, 2], [500, 700], 48, 6, 1),             # 48 rows: two copies, pages that do not divide a tile
+    ([16, 0, 9], [200, 50, 130], 128, 8, 1),    # 128 rows, an empty sequence between
+    ([7, 25], [40, 2000], 256, 5, 1),           # 125 rows, group of five
+    ([1] * 40, [17 + 31 * i for i in range(40)], 8, 4, 4),
+    ([128], [128], 16, 1, 1),
+]
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("case", FEW)
+def test_few_rows(case, d):
+    new, lens, page, hq, hkv = case
+    run(new, lens, page, hq, hkv, d, seed=sum(lens) + d)
+
+
+CHUNKS = [
+    ([129], [129], 16, 1, 1),
+    ([300], [300], 64, 4, 2),
+    ([200, 1, 0, 33], [1000, 77, 10, 33], 16, 8, 2),
+    ([64, 64], [64, 3000], 48, 12, 4),          # groups of three
+    ([257, 1, 1], [400, 2500, 1], 128, 4, 1),
+    ([40], [5000], 256, 10, 2),                 # groups of five, few units: cut along the keys
+    ([140, 3], [141, 4000], 8, 2, 2),
+]
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("case", CHUNKS)
+def test_chunks(case, d):
+    new, lens, page, hq, hkv = case
+    run(new, lens, page, hq, hkv, d, seed=sum(lens) + d)
+
+
+@pytest.mark.parametrize("new", [[3, 5], [130, 70]])
+@pytest.mark.parametrize("d", [64, 128])
+def test_not_causal(new, d):
+    run(new, [333, 700], 32, 4, 2, d, causal=False, seed=5)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new,lens", [([4, 2], [2, 0]), ([150, 140, 1], [20, 0, 0]), ([3, 1], [0, 5])])
+def test_rows_without_keys(new, lens, d):
+    # New tokens at places below 0 (a cache shorter than its new tokens) and empty caches: O = 0, L = -inf.
+    o, lse = run(new, lens, 16, 4, 2, d, seed=9)
+    n, m = new[0], lens[0]
+    assert (o[:n - m] == 0).all() and torch.isneginf(lse[:, :n - m]).all()
+    run(new, lens, 16, 4, 2, d, causal=False, seed=9)
+
+
+@pytest.mark.parametrize("new", [[1, 1], [100, 60]])
+def test_a_loose_bound_on_new_tokens(new):
+    # max_q above the longest sequence may take the other kernel; the result is the same to rounding.
+    run(new, [300, 400], 16, 4, 2, 128, seed=11, max_q=200)
+
+
+@pytest.mark.parametrize("new", [[2, 3], [150, 20]])
+@pytest.mark.parametrize("d", [64, 128])
+def test_strided_views(new, d):
+    lens, hq, hkv = [200, 333], 4, 2
+    cache = Cache(3, lens, 16, hkv, d, token_major=True)
+    kp, vp, table, ln = cache.cuda()
+    cu = offsets(new)
+    T = int(cu[-1])
+    fused = normal(4, T, hq + 2 * hkv, d).cuda()   # q is a slice of a fused projection
+    wide = torch.full((2, table.shape[1] + 5), 2 ** 30, dtype=torch.int32, device="cuda")
+    wide[:, :table.shape[1]] = table
+    out = torch.full((hq, T + 3, d), 7.0, dtype=torch.bfloat16, device="cuda")  # head-major output
+    lse = torch.empty(hq, T, device="cuda")
+    ws = torch.empty(fa.fa_paged_fwd_workspace_bytes(2, T, max(new), hq, hkv, d, 16, table.shape[1]),
+                     dtype=torch.uint8, device="cuda")
+    fa.fa_paged_fwd(fused[:, :hq], kp, vp, out.transpose(0, 1)[:T], lse, wide[:, :table.shape[1]], ln,
+                    torch.from_numpy(cu).cuda(), max(new), True, 0.125, ws)
+    done()
+    ref = oracle.paged_ref(to_f64(fused[:, :hq]), to_f64(cache.k), to_f64(cache.v), cache.table, cache.lens, cu, True,
+                           0.125)
+    assert_forward(out.transpose(0, 1)[:T], lse, *ref)
+    assert (out[:, T:] == 7.0).all()
+
+
+@pytest.mark.parametrize("lens,max_q", [([100, 200], 4), ([300, 150], 140)])
+def test_rows_outside_the_sequences_stay(lens, max_q):
+    # Offsets that start behind row 0 and end before the last: those rows are left as they were.
+    new = [min(4, max_q), max_q]
+    cache = Cache(21, lens, 16, 2, 64)
+    kp, vp, table, ln = cache.cuda()
+    cu = offsets(new) + 3
+    T = int(cu[-1]) + 5
+    q = normal(22, T, 4, 64)
+    q[:3] = q[-5:] = float("nan")
+    o = torch.full((T, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((4, T), 7.0, device="cuda")
+    ws = torch.empty(fa.fa_paged_fwd_workspace_bytes(2, T, max_q, 4, 2, 64, 16, table.shape[1]), dtype=torch.uint8,
+                     device="cuda")
+    fa.fa_paged_fwd(q.cuda(), kp, vp, o, lse, table, ln, torch.from_numpy(cu).cuda(), max_q, True, 0.125, ws)
+    done()
+    assert_forward(o, lse, *oracle.paged_ref(to_f64(q), to_f64(cache.k), to_f64(cache.v), cache.table, cache.lens, cu,
+                                             True, 0.125))
+    assert (o[:3] == 7).all() and (o[-5:] == 7).all() and (lse[:, :3] == 7).all() and (lse[:, -5:] == 7).all()
+
+
+def test_single_tokens_without_offsets_and_shared_pages():
+    # No offsets: one token each. Both sequences read the same pages.
+    cache = Cache(31, [500], 16, 2, 128)
+    kp, vp, table, _ = cache.cuda()
+    table2 = table.repeat(3, 1)
+    lens = np.array([500, 123, 500], dtype=np.int32)
+    q = normal(32, 3, 8, 128)
+    o, lse = fa.attention_paged(q.cuda(), kp, vp, table2, torch.from_numpy(lens).cuda(), scale=0.125)
+    done()
+    ref = oracle.paged_ref(to_f64(q), to_f64(cache.k), to_f64(cache.v), np.repeat(cache.table, 3, 0), lens,
+                           offsets([1, 1, 1]), True, 0.125)
+    assert_forward(o, lse, *ref)
+
+
+@pytest.mark.parametrize("rows", [[2, 3], [140, 150]])
+@pytest.mark.parametrize("break_", ["len", "negative_len", "order", "end", "max_q"])
+def test_out_of_range_lengths_are_reported_and_nothing_is_written(rows, break_):
+    cache = Cache(41, [200, 300], 16, 2, 64)
+    kp, vp, table, ln = cache.cuda()
+    cu = offsets(rows)
+    T, max_q = int(cu[-1]), max(rows)
+    if break_ == "len":
+        ln[1] = table.shape[1] * 16 + 1
+    elif break_ == "negative_len":
+        ln[0] = -1
+    elif break_ == "order":
+        cu[1] = T + 1
+    elif break_ == "end":
+        cu[2] = T + 1
+    else:
+        max_q -= 1
+    q = normal(42, T, 4, 64).cuda()
+    o = torch.full((T, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((4, T), 7.0, device="cuda")
+    ws = torch.empty(fa.fa_paged_fwd_workspace_bytes(2, T, max_q, 4, 2, 64, 16, table.shape[1]), dtype=torch.uint8,
+                     device="cuda")
+    fa.fa_paged_fwd(q, kp, vp, o, lse, table, ln, torch.from_numpy(cu).cuda(), max_q, True, 0.125, ws)
+    assert fa.fa_check_device_error() == fa.FA_ERR_DATA
+    assert fa.fa_check_device_error() == fa.FA_OK
+    assert (o == 7).all() and (lse == 7).all()
+
+
+@pytest.mark.parametrize("new", [1, 150])
+@pytest.mark.parametrize("bad", [-1, 2 ** 30])
+def test_a_page_outside_the_pool_is_read_as_zeros_and_reported(new, bad):
+    cache = Cache(51, [300], 16, 2, 64)
+    kp, vp, table, ln = cache.cuda()
+    table[0, 3] = bad
+    q = normal(52, new, 4, 64)
+    o, lse = fa.attention_paged(q.cuda(), kp, vp, table, ln, torch.from_numpy(offsets([new])).cuda(), new, True, 0.125)
+    assert fa.fa_check_device_error() == fa.FA_ERR_DATA
+    page = cache.table[0, 3]
+    cache.k[page] = cache.v[page] = 0
+    assert_forward(o, lse, *oracle.paged_ref(to_f64(q), to_f64(cache.k), to_f64(cache.v), cache.table, cache.lens,
+                                             offsets([new]), True, 0.125))
+
+
+@pytest.mark.parametrize("new", [[1, 1], [90, 100]])
+def test_captured_call_replays_on_grown_sequences(new):
+    page, hq, hkv, d = 16, 4, 2, 64
+    cache = Cache(61, [700, 900], page, hkv, d)
+    kp, vp, table, ln = cache.cuda()
+    q = normal(62, sum(new), hq, d).cuda()
+    cu = torch.from_numpy(offsets(new)).cuda()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        fa.attention_paged(q, kp, vp, table, ln, cu, max(new), True, 0.125)
+    torch.cuda.current_stream().wait_stream(s)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        o, lse = fa.attention_paged(q, kp, vp, table, ln, cu, max(new), True, 0.125)
+    for lens in ([700, 900], [150, 899], [101, 333]):
+        ln.copy_(torch.tensor(lens, dtype=torch.int32))
+        g.replay()
+        done()
+        want = fa.attention_paged(q, kp, vp, table, ln, cu, max(new), True, 0.125)
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+        ref = oracle.paged_ref(to_f64(q), to_f64(cache.k), to_f64(cache.v), cache.table, np.array(lens), offsets(new),
+                               True, 0.125)
+        assert_forward(o, lse, *ref)
+
+
+def test_on_another_stream():
+    cache = Cache(71, [700, 900], 16, 2, 128)
+    kp, vp, table, ln = cache.cuda()
+    q = normal(72, 2, 8, 128).cuda()
+    want = fa.attention_paged(q, kp, vp, table, ln, scale=0.125)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for stream in (s, s.cuda_stream):
+        got = fa.attention_paged(q, kp, vp, table, ln, scale=0.125, stream=stream)
+        s.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_offsets_past_32_bits():
+    # A pool of more than 2^32 bytes per tensor and 2^31 elements: pages at its end.
+    page, hkv, d = 256, 8, 128
+    n_pages = (1 << 31) // (page * hkv * d) + 9
+    k = torch.zeros(n_pages, hkv, page, d, dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    small = Cache(81, [1000], page, hkv, d, spare=0)
+    table = small.table + (n_pages - small.n_pages)
+    k[n_pages - small.n_pages:] = small.k.cuda()
+    v[n_pages - small.n_pages:] = small.v.cuda()
+    for new in (1, 140):
+        q = normal(82, new, 16, d)
+        o, lse = fa.attention_paged(q.cuda(), k, v, torch.from_numpy(table).cuda(),
+                                    torch.from_numpy(small.lens).cuda(), torch.from_numpy(offsets([new])).cuda(), new,
+                                    True, 0.125)
+        done()
+        assert_forward(o, lse, *oracle.paged_ref(to_f64(q), to_f64(small.k), to_f64(small.v), small.table, small.lens,
+                                                 offsets([new]), True, 0.125))
