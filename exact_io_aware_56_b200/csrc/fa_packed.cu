@@ -107,7 +107,7 @@ struct PkBars {
   uint64_t k_full[3], v_full[2], v_land[2], k_empty[3], v_empty[2];
   uint64_t s_full[2], p_ready[2][2], o_final[2];
   uint64_t s_free, pv_done;
-  uint64_t epi_full[2], epi_free[2];
+  uint64_t epi_full[2][2], epi_free[2];  // epi_full: [tile][staging box]
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
@@ -168,7 +168,8 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, PkCfg<D>::kMinBlocks)
       mbar_init(&bars->p_ready[t][0], kBM);
       mbar_init(&bars->p_ready[t][1], kBM);
       mbar_init(&bars->o_final[t], 1);
-      mbar_init(&bars->epi_full[t], kBM);
+      mbar_init(&bars->epi_full[t][0], kBM);
+      mbar_init(&bars->epi_full[t][1], kBM);
       mbar_init(&bars->epi_free[t], 1);
     }
     mbar_init(&bars->s_free, kBM);
@@ -559,9 +560,11 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, PkCfg<D>::kMinBlocks)
             for (int cc = 0; cc < 8; ++cc)
               *reinterpret_cast<uint4*>(st + rw * 128 + ((cc ^ (rw & 7)) << 4)) = pack8(oo + 8 * cc, resid);
             fence_proxy_async_smem();
-            mbar_arrive(&bars->epi_full[t]);
+            // A barrier for each box: a fast warp arrives for the second
+            // before a slow one has for the first.
+            mbar_arrive(&bars->epi_full[t][i & 1]);
             // (On a timeout every lane leaves at the next wait for epi_free.)
-            if (issuer && (ok = wait_bar(&bars->epi_full[t], i & 1, w))) {
+            if (issuer && (ok = wait_bar(&bars->epi_full[t][i & 1], (i >> 1) & 1, w))) {
               tma_store_4d(resid ? &tmR : &tmO, st, x * 64, 0, tok_base + tok0, kvh);
               bulk_commit();
               if (i + 1 < jobs && i + 1 >= 2) {

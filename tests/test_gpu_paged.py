@@ -247,3 +247,19 @@ def test_offsets_past_32_bits():
         done()
         assert_forward(o, lse, *oracle.paged_ref(to_f64(q), to_f64(small.k), to_f64(small.v), small.table, small.lens,
                                                  offsets([new]), True, 0.125))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_results_repeat(d):
+    # Chunks beside single tokens, some units cut along the keys, some whole: every run gives the same bits.
+    new, lens = [200, 130, 1, 33], [700, 2048, 3000, 33]
+    cache = Cache(91, lens, 16, 4, d)
+    kp, vp, table, ln = cache.cuda()
+    q = normal(92, sum(new), 16, d).cuda()
+    cu = torch.from_numpy(offsets(new)).cuda()
+    first = None
+    for _ in range(40):
+        got = fa.attention_paged(q, kp, vp, table, ln, cu, max(new), True, 0.125)
+        first = first or got
+        assert torch.equal(got[0], first[0]) and torch.equal(got[1], first[1])
+    done()
