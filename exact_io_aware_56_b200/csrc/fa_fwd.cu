@@ -200,7 +200,7 @@ struct FwdBars {
   uint64_t k_full[4], v_full[4], k_empty[4], v_empty[4];
   uint64_t s_full[2], p_ready[2][2], o_final[2];  // p_ready: [Q tile][half of P]
   uint64_t s_free[2], pv_done[2];  // separate-P schedule (d = 64) only
-  uint64_t epi_full[2], epi_free[2];  // output staging (see the epilogue)
+  uint64_t epi_full[2][2], epi_free[2];  // output staging (see the epilogue); epi_full: [Q tile][slot]
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
@@ -293,7 +293,8 @@ __global__ void __launch_bounds__(FwdCfg<D, F8, T>::kThreads, FwdCfg<D, F8, T>::
       mbar_init(&bars->o_final[t], 1);
       mbar_init(&bars->s_free[t], kBM);
       mbar_init(&bars->pv_done[t], 1);
-      mbar_init(&bars->epi_full[t], kBM);
+      mbar_init(&bars->epi_full[t][0], kBM);
+      mbar_init(&bars->epi_full[t][1], kBM);
       mbar_init(&bars->epi_free[t], 1);
     }
     mbar_init(&bars->drain, 1);
@@ -814,9 +815,11 @@ __global__ void __launch_bounds__(FwdCfg<D, F8, T>::kThreads, FwdCfg<D, F8, T>::
             *reinterpret_cast<uint4*>(slot + r * 128 + ((cc ^ (r & 7)) << 4)) = v;
           }
           fence_proxy_async_smem();
-          mbar_arrive(&bars->epi_full[t]);
+          // A barrier for each slot: a fast warp arrives for the second box
+          // before a slow one has for the first.
+          mbar_arrive(&bars->epi_full[t][i % kSlots]);
           if (issuer) {
-            if (!(ok = wait_bar(&bars->epi_full[t], i & 1, w))) break;
+            if (!(ok = wait_bar(&bars->epi_full[t][i % kSlots], (i / kSlots) & 1, w))) break;
             tma_store_3d(resid ? &tmR : &tmO, slot, x * 64, qt0, bh);
             bulk_commit();
             if (i + 1 < jobs && i + 1 >= kSlots) {
