@@ -9,6 +9,7 @@ no CPU fallback, and a missing library or device raises ``RuntimeError``.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -116,7 +117,8 @@ def status_string(status: int) -> str:
 
 def _stream(stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # The current stream's handle, without building a Stream object (3 us).
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -300,8 +302,13 @@ def _check_view(name, t, dtype, shape, dev):
 
 
 def _rows(name, t, shape, dev):
-    st = _check_view(name, t, torch.bfloat16, shape, dev)
-    return Rows(t.data_ptr(), st[0], st[1])
+    """``fa_rows`` of a bf16 [T, H, d] view. (The usual case is looked at first: a call marshals up to nine.)"""
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.get_device() == dev and t.shape == shape):
+        _check_view(name, t, torch.bfloat16, shape, dev)
+    ts, hs, ds = t.stride()
+    if ds != 1:
+        _check_view(name, t, torch.bfloat16, shape, dev)
+    return Rows(t.data_ptr(), ts, hs)
 
 
 def _pages(name, t, shape, dev):
@@ -432,15 +439,22 @@ def fa_paged_fwd(q, k_pages, v_pages, o, lse, block_table, seq_lens, cu_seqlens,
                            int(bool(causal)), float(scale), wa, wb, _stream(stream)), "fa_paged_fwd")
 
 
+@functools.lru_cache(maxsize=64)
+def _section_array(sections):
+    return (ctypes.c_int * len(sections))(*sections)
+
+
 def _sections(sections, inv_freq):
+    """(sections, their C array, pairs)."""
     if inv_freq is None:
         if sections is not None and len(sections):
             raise ValueError("sections need inv_freq")
         return 0, None, 0
-    sections = [inv_freq.numel()] if sections is None else [int(n) for n in sections]
-    if sum(sections) != inv_freq.numel():
-        raise ValueError(f"sections {sections} must sum to inv_freq's {inv_freq.numel()} pairs")
-    return len(sections), (ctypes.c_int * len(sections))(*sections), inv_freq.numel()
+    pairs = inv_freq.numel()
+    sections = (pairs,) if sections is None else tuple(map(int, sections))
+    if sum(sections) != pairs:
+        raise ValueError(f"sections {sections} must sum to inv_freq's {pairs} pairs")
+    return len(sections), _section_array(sections), pairs
 
 
 def fa_rope(q, k, q_out, k_out, positions, inv_freq, sections=None, interleaved: bool = False, inverse: bool = False,
@@ -581,28 +595,26 @@ def attention_forward_fp8(q, k, v, causal: bool, scale: float | None = None, str
     return o, lse, (q8, sq, k8, sk, v8, sv)
 
 
-class _Allocate:
-    """Memory for one call on ``stream``: new tensors belong to that stream, and the caching allocator learns that
-    the call's inputs are used on it."""
+def _side_stream(stream, *inputs):
+    """For a call on a stream other than the current one: that stream, after telling the caching allocator that the
+    inputs are used on it; else ``None``."""
+    if stream is None:
+        return None
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream))
+    if s == torch.cuda.current_stream():
+        return None
+    for t in inputs:
+        if isinstance(t, torch.Tensor) and t.is_cuda:
+            t.record_stream(s)
+    return s
 
-    def __init__(self, stream, *inputs):
-        self.stream = None
-        if stream is not None:
-            s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream))
-            if s != torch.cuda.current_stream():
-                self.stream = s
-                for t in inputs:
-                    if isinstance(t, torch.Tensor) and t.is_cuda:
-                        t.record_stream(s)
 
-    def empty(self, shape, dtype, device):
-        if self.stream is None:
-            return torch.empty(shape, dtype=dtype, device=device)
-        with torch.cuda.stream(self.stream):
-            return torch.empty(shape, dtype=dtype, device=device)
-
-    def bytes(self, n, device):
-        return self.empty(max(16, n), torch.uint8, device)
+def _empty(like, shape, dtype=None, side=None):
+    """New contiguous memory, on a side stream where there is one, so that it belongs to that stream."""
+    if side is None:
+        return like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(side):
+        return like.new_empty(shape, dtype=dtype)
 
 
 def attention_packed_forward(q, k, v, cu_seqlens, causal: bool, scale: float | None = None, stream=None,
@@ -614,12 +626,13 @@ def attention_packed_forward(q, k, v, cu_seqlens, causal: bool, scale: float | N
     """
     T, Hq, d = _three("q", q)
     scale = d ** -0.5 if scale is None else scale
-    new = _Allocate(stream, q, k, v, cu_seqlens, workspace)
+    side = _side_stream(stream, q, k, v, cu_seqlens, workspace)
     if workspace is None:
-        workspace = new.bytes(fa_packed_fwd_workspace_bytes(cu_seqlens.numel() - 1, T, Hq, k.shape[1], d), q.device)
-    o = new.empty((T, Hq, d), q.dtype, q.device)
-    lse = new.empty((Hq, T), torch.float32, q.device)
-    o_resid = new.empty((T, Hq, d), q.dtype, q.device) if residual else None
+        need = fa_packed_fwd_workspace_bytes(cu_seqlens.numel() - 1, T, Hq, _three("k", k)[1], d)
+        workspace = _empty(q, max(16, need), torch.uint8, side)
+    o = _empty(q, (T, Hq, d), None, side)
+    lse = _empty(q, (Hq, T), torch.float32, side)
+    o_resid = _empty(q, (T, Hq, d), None, side) if residual else None
     fa_packed_fwd(q, k, v, o, lse, cu_seqlens, causal, scale, workspace, stream, o_resid=o_resid)
     return (o, lse, o_resid) if residual else (o, lse)
 
@@ -630,12 +643,13 @@ def attention_packed_backward(q, k, v, o, dout, lse, cu_seqlens, causal: bool, s
     T, Hq, d = _three("q", q)
     Hkv = _three("k", k)[1]
     scale = d ** -0.5 if scale is None else scale
-    new = _Allocate(stream, q, k, v, o, dout, lse, cu_seqlens, o_resid, workspace)
+    side = _side_stream(stream, q, k, v, o, dout, lse, cu_seqlens, o_resid, workspace)
     if workspace is None:
-        workspace = new.bytes(fa_packed_bwd_workspace_bytes(cu_seqlens.numel() - 1, T, Hq, Hkv, d), q.device)
-    dq = new.empty((T, Hq, d), q.dtype, q.device)
-    dk = new.empty((T, Hkv, d), q.dtype, q.device)
-    dv = new.empty((T, Hkv, d), q.dtype, q.device)
+        need = fa_packed_bwd_workspace_bytes(cu_seqlens.numel() - 1, T, Hq, Hkv, d)
+        workspace = _empty(q, max(16, need), torch.uint8, side)
+    dq = _empty(q, (T, Hq, d), None, side)
+    dk = _empty(q, (T, Hkv, d), None, side)
+    dv = _empty(q, (T, Hkv, d), None, side)
     fa_packed_bwd(q, k, v, o, dout, lse, dq, dk, dv, cu_seqlens, causal, scale, workspace, stream, o_resid=o_resid)
     return dq, dk, dv
 
@@ -651,13 +665,13 @@ def attention_paged(q, k_pages, v_pages, block_table, seq_lens, cu_seqlens=None,
     scale = d ** -0.5 if scale is None else scale
     if max_q is None:
         max_q = 1 if cu_seqlens is None else max(1, T)
-    new = _Allocate(stream, q, k_pages, v_pages, block_table, seq_lens, cu_seqlens, workspace)
+    side = _side_stream(stream, q, k_pages, v_pages, block_table, seq_lens, cu_seqlens, workspace)
     if workspace is None:
         S = T if cu_seqlens is None else cu_seqlens.numel() - 1
-        workspace = new.bytes(fa_paged_fwd_workspace_bytes(S, T, max_q, Hq, k_pages.shape[1], d, k_pages.shape[2],
-                                                           block_table.shape[1]), q.device)
-    o = new.empty((T, Hq, d), q.dtype, q.device)
-    lse = new.empty((Hq, T), torch.float32, q.device)
+        need = fa_paged_fwd_workspace_bytes(S, T, max_q, Hq, k_pages.shape[1], d, k_pages.shape[2], block_table.shape[1])
+        workspace = _empty(q, max(16, need), torch.uint8, side)
+    o = _empty(q, (T, Hq, d), None, side)
+    lse = _empty(q, (Hq, T), torch.float32, side)
     fa_paged_fwd(q, k_pages, v_pages, o, lse, block_table, seq_lens, cu_seqlens, max_q, causal, scale, workspace, stream)
     return o, lse
 
@@ -665,8 +679,8 @@ def attention_paged(q, k_pages, v_pages, block_table, seq_lens, cu_seqlens=None,
 def paged_append(k, v, k_pages, v_pages, block_table, seq_lens, cu_seqlens=None, q=None, positions=None, inv_freq=None,
                  sections=None, interleaved: bool = False, stream=None):
     """Runs :func:`fa_paged_append`; returns the (turned) ``q`` in a new tensor, or ``None`` without ``q``."""
-    new = _Allocate(stream, q, k, v, k_pages, v_pages, block_table, seq_lens, cu_seqlens, positions, inv_freq)
-    q_out = None if q is None else new.empty(_three("q", q), q.dtype, q.device)
+    side = _side_stream(stream, q, k, v, k_pages, v_pages, block_table, seq_lens, cu_seqlens, positions, inv_freq)
+    q_out = None if q is None else _empty(q, _three("q", q), None, side)
     fa_paged_append(q, k, v, q_out, k_pages, v_pages, block_table, seq_lens, cu_seqlens, positions, inv_freq, sections,
                     interleaved, stream)
     return q_out
@@ -674,8 +688,8 @@ def paged_append(k, v, k_pages, v_pages, block_table, seq_lens, cu_seqlens=None,
 
 def rope(q, k, positions, inv_freq, sections=None, interleaved: bool = False, inverse: bool = False, stream=None):
     """Allocates the outputs and runs :func:`fa_rope`; returns ``(q_out, k_out)`` (``None`` for ``None``)."""
-    new = _Allocate(stream, q, k, positions, inv_freq)
-    q_out = None if q is None else new.empty(_three("q", q), q.dtype, q.device)
-    k_out = None if k is None else new.empty(_three("k", k), k.dtype, k.device)
+    side = _side_stream(stream, q, k, positions, inv_freq)
+    q_out = None if q is None else _empty(q, _three("q", q), None, side)
+    k_out = None if k is None else _empty(k, _three("k", k), None, side)
     fa_rope(q, k, q_out, k_out, positions, inv_freq, sections, interleaved, inverse, stream)
     return q_out, k_out
