@@ -194,7 +194,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   int nq = a.nq;
   if constexpr (VAR) {
     static_assert(MASK != 2, "packed sequences: no mask or causal");
-    pdl_wait();  // the plan and the D_i are written
     const int item_no = blockIdx.x / a.Hkv;
     if (item_no >= a.head->items) return;
     const PlanItem item = a.items[item_no];
@@ -837,16 +836,20 @@ cudaError_t launch_bwd_t(const AttnShape& s, const CUtensorMap& tq, const CUtens
 
 // D_i and the zeroed dQ accumulator of packed rows: one warp per (head, row),
 // rows outside [cu[0], cu[S]) left out. dsum and dq_acc are [Hq][T] and
-// [Hq][T][D].
+// [Hq][T][D]. Block 0 lists the main kernel's work meanwhile.
 template <int D>
-__global__ void __launch_bounds__(256) packed_pre_kernel(Rows o, Rows resid, Rows dout, float* __restrict__ dsum,
+__global__ void __launch_bounds__(256) packed_pre_kernel(const PlanArgs plan, Rows o, Rows resid, Rows dout, float* __restrict__ dsum,
                                                          float* __restrict__ dq_acc, const int* __restrict__ cu, int S,
                                                          int T, int Hq) {
-  pdl_launch_dependents();
+  if (blockIdx.x == 0) {
+    __shared__ PlanShared sh;
+    plan_block<256>(plan, sh);
+    return;
+  }
   const int t0 = max(0, cu[0]), t1 = min(T, cu[S]);
-  const long long warp_g = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+  const long long warp_g = (static_cast<long long>(blockIdx.x - 1) * blockDim.x + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
-  const long long nwarps = (static_cast<long long>(gridDim.x) * blockDim.x) >> 5;
+  const long long nwarps = (static_cast<long long>(gridDim.x - 1) * blockDim.x) >> 5;
   for (long long e = warp_g; e < static_cast<long long>(T) * Hq; e += nwarps) {
     const int t = static_cast<int>(e / Hq), h = static_cast<int>(e % Hq);  // heads of a token are neighbours in memory
     if (t < t0 || t >= t1) continue;
@@ -914,7 +917,7 @@ struct PackedBwdLayout {
 PackedBwdLayout packed_bwd_layout(const SeqShape& s) {
   PackedBwdLayout x;
   x.max_items = plan_max_units(s.S, s.T, kKT);
-  x.plan = plan_layout(s.S, x.max_items, 0);
+  x.plan = plan_layout(x.max_items, 0);
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   x.off_d = up(x.plan.bytes);
   const size_t rows = static_cast<size_t>(s.T) * s.Hq;
@@ -946,16 +949,12 @@ cudaError_t launch_packed_bwd_t(const SeqShape& s, const PackedBwdLayout& x, con
   p.causal = s.causal;
   p.backward = 1;
   p.heads = s.Hkv;
-  p.upre = reinterpret_cast<int*>(ws + x.plan.upre);
   p.head = reinterpret_cast<PlanHeader*>(ws + x.plan.head);
   p.items = reinterpret_cast<PlanItem*>(ws + x.plan.items);
-  p.slots = reinterpret_cast<int*>(ws + x.plan.slots);
   p.err = ctl.err;
-  plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const long long rows = static_cast<long long>(s.T) * s.Hq;
-  packed_pre_kernel<D><<<grid_for(rows, 8, 148 * 64), 256, 0, stream>>>(o, resid, dout, dsum, dq_acc, s.cu, s.S, s.T,
-                                                                       s.Hq);
+  packed_pre_kernel<D><<<1 + grid_for(rows, 8, 148 * 64), 256, 0, stream>>>(p, o, resid, dout, dsum, dq_acc, s.cu, s.S,
+                                                                            s.T, s.Hq);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   BwdArgs a{};
   a.lse = lse;

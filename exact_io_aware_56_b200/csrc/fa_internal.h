@@ -169,6 +169,23 @@ inline int page_box(int page) {
   return b;
 }
 
+// Launches a kernel that may start beside the one before it on the stream
+// (programmatic dependent launch) and waits for it with pdl_wait().
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
+
 // True when every sequence's query rows of a KV head fit one 128-row tile:
 // these calls take the few-row kernel (fa_paged.cu), the others the prompt
 // kernel (fa_packed.cu).

@@ -114,6 +114,13 @@ struct PkBars {
 };
 static_assert(sizeof(PkBars) <= 512, "barrier block exceeds its shared-memory reservation");
 
+constexpr int kPlanThreads = 512;
+__global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PlanArgs a) {
+  __shared__ PlanShared sh;
+  pdl_launch_dependents();
+  plan_block<kPlanThreads>(a, sh);
+}
+
 template <int D, bool PAGED>
 __global__ void __launch_bounds__(PkCfg<D>::kThreads, PkCfg<D>::kMinBlocks)
     packed_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -131,26 +138,6 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, PkCfg<D>::kMinBlocks)
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-
-  pdl_launch_dependents();
-  pdl_wait();  // the plan is written
-  const int item_no = blockIdx.x / a.Hkv;
-  if (item_no >= a.head->items) return;
-  const int kvh = blockIdx.x - item_no * a.Hkv;
-  const PlanItem item = a.items[item_no];
-  const int tok_base = a.cu ? a.cu[item.seq] : item.seq;  // the sequence's first row
-  const int n_tok = a.cu ? a.cu[item.seq + 1] - tok_base : 1;
-  const int len = PAGED ? a.lens[item.seq] : n_tok;
-  const int off = len - n_tok;  // place of the first new token
-  // Tile t: tokens [tok0 + t TT, ...), key tiles [j0, j0 + n_t).
-  int n_t[2] = {0, 0}, tok_t[2];
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    tok_t[t] = item.tok0 + t * a.TT;
-    if (t < T && tok_t[t] < n_tok)
-      n_t[t] = max(0, min(item.j1, plan_fwd_tiles(n_tok, len, tok_t[t], a.TT, a.causal)) - item.j0);
-  }
-  const int n = max(n_t[0], n_t[1]);  // stream length
 
   if (threadIdx.x == 0) {
     mbar_init(&bars->q_full, 1);
@@ -185,6 +172,30 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, PkCfg<D>::kMinBlocks)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // Everything above ran beside the plan.
+  pdl_launch_dependents();
+  pdl_wait();
+  const int item_no = blockIdx.x / a.Hkv;
+  if (item_no >= a.head->items) {
+    if (warp == C::kMmaWarp) tmem_dealloc(bars->tmem_base, C::kTmemCols);
+    return;
+  }
+  const int kvh = blockIdx.x - item_no * a.Hkv;
+  const PlanItem item = a.items[item_no];
+  const int tok_base = a.cu ? a.cu[item.seq] : item.seq;  // the sequence's first row
+  const int n_tok = a.cu ? a.cu[item.seq + 1] - tok_base : 1;
+  const int len = PAGED ? a.lens[item.seq] : n_tok;
+  const int off = len - n_tok;  // place of the first new token
+  // Tile t: tokens [tok0 + t TT, ...), key tiles [j0, j0 + n_t).
+  int n_t[2] = {0, 0}, tok_t[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    tok_t[t] = item.tok0 + t * a.TT;
+    if (t < T && tok_t[t] < n_tok)
+      n_t[t] = max(0, min(item.j1, plan_fwd_tiles(n_tok, len, tok_t[t], a.TT, a.causal)) - item.j0);
+  }
+  const int n = max(n_t[0], n_t[1]);  // stream length
+
   const uint32_t tmem = bars->tmem_base;
   const Watch w{&bars->abort, a.ctl.err, a.ctl.budget_ns};
   auto all = [](bool b) { return __all_sync(0xffffffffu, b); };
@@ -677,26 +688,11 @@ Layout make_layout(const SeqShape& s, const CacheShape* c, int ctas) {
     if (x.max_splits > units) x.max_splits = static_cast<int>(units);
     x.max_items += 4LL * ctas / s.Hkv + 1;
   }
-  x.plan = plan_layout(s.S, x.max_items, x.max_splits);
+  x.plan = plan_layout(x.max_items, x.max_splits);
   x.off_o = x.plan.bytes;
   x.off_l = x.off_o + static_cast<size_t>(x.max_parts) * tiles * kBM * s.d * 4;
   x.bytes = x.off_l + static_cast<size_t>(x.max_parts) * tiles * kBM * 4;
   return x;
-}
-
-template <typename... P, typename... A>
-cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
 }
 
 template <int D, bool PAGED>
@@ -729,7 +725,6 @@ cudaError_t launch_t(const SeqShape& s, const CacheShape* c, const Layout& x, co
   p.causal = s.causal;
   p.heads = s.Hkv;
   p.split_ctas = x.max_parts > 0 ? sms : 0;
-  p.upre = reinterpret_cast<int*>(ws + x.plan.upre);
   p.head = reinterpret_cast<PlanHeader*>(ws + x.plan.head);
   p.items = reinterpret_cast<PlanItem*>(ws + x.plan.items);
   p.slots = reinterpret_cast<int*>(ws + x.plan.slots);
@@ -764,7 +759,7 @@ cudaError_t launch_t(const SeqShape& s, const CacheShape* c, const Layout& x, co
   a.ctl = ctl;
   const long long grid = x.max_items * s.Hkv;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
+  packed_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   e = launch_dependent(kern, dim3(static_cast<unsigned>(grid)), C::kThreads, C::kSmemBytes, stream, tq, tk, tv, to, tr,
                        a);

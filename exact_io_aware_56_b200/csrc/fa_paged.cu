@@ -13,9 +13,9 @@
 // SM ("stream-K"): one wave, no tail, whatever the mix of lengths. A run's
 // part of a unit is a segment; a second kernel merges a unit's segments by
 // their logsumexp. The lengths live on the device, so that a captured graph
-// can be replayed as sequences grow: a one-block kernel first sums the units'
-// tiles (and checks lengths and offsets); the three kernels are chained by
-// programmatic dependent launch.
+// can be replayed as sequences grow: every warp sums the sequences' tiles
+// itself (32 sequences per step), which for tens of sequences costs less
+// than a kernel before this one (measured: 3.5 us of 109 at 32 sequences).
 //
 // A tile's keys come by TMA, one box per page part (page_box() rows); page
 // numbers are looked up by the producer warp's lanes in parallel. Slots
@@ -77,14 +77,14 @@ struct Cfg {
 };
 
 struct Args {
-  float* part_o;              // [S * Hkv + G][RHO][rv][D] partial O / l
-  float* part_l;              // [S * Hkv + G][RHO][rv] partial logsumexp (natural log, -inf: no key)
-  const long long* tile_pre;  // [S + 1] tiles of a unit of each sequence, summed
+  float* part_o;        // [S * Hkv + G][RHO][rv][D] partial O / l
+  float* part_l;        // [S * Hkv + G][RHO][rv] partial logsumexp (natural log, -inf: no key)
+  long long* tile_pre;  // [S + 1] tiles of a unit of each sequence, summed (written for the merge)
   const int* cu;
   const int* lens;
   const int* table;
-  long long table_stride;
-  int S, Hkv, r, n_pages, page, pb, causal, rv, q_tokens;
+  long long table_stride, max_len;
+  int S, T, max_q, Hkv, r, n_pages, page, pb, causal, rv, q_tokens;
   float scale_log2;
   LaunchCtl ctl;
 };
@@ -102,101 +102,104 @@ static_assert(sizeof(Bars) <= 384, "barrier block exceeds its shared-memory rese
 
 // No more runs than tiles, so that none is empty (the merge counts on it).
 __device__ __forceinline__ int runs_of(long long W, int ctas) { return W < ctas ? (W < 1 ? 1 : static_cast<int>(W)) : ctas; }
-__device__ __forceinline__ long long run_lo(long long c, long long W, int G) { return c * W / G; }
+// First tile of run c of G; in 32 bits where they hold it (W G < 2^31).
+__device__ __forceinline__ long long run_lo(int c, long long W, int G) {
+  if (W <= (1 << 22)) return static_cast<unsigned>(c) * static_cast<unsigned>(W) / static_cast<unsigned>(G);
+  return c * W / G;
+}
 // The run holding tile t: the largest c with run_lo(c) <= t.
 __device__ __forceinline__ int run_of(long long t, long long W, int G) {
+  if (W <= (1 << 22)) {
+    const unsigned w = static_cast<unsigned>(W);
+    return static_cast<int>(((static_cast<unsigned>(t) + 1) * G + w - 1) / w) - 1;
+  }
   return static_cast<int>(((t + 1) * G + W - 1) / W) - 1;
+}
+
+// Tiles of a unit of sequence b: one at least where there are new tokens.
+__device__ __forceinline__ int seq_tiles(const Args& a, int b, bool& bad) {
+  const SeqRange s = seq_range(a.cu, a.lens, b, a.T, a.max_q, a.max_len);
+  bad |= s.bad;
+  return s.n > 0 ? max(1, (s.len + kT - 1) / kT) : 0;
 }
 
 // Walks the tiles of a run [lo, hi): sequence b, KV head kvh, tile j of the
 // unit's T, segment e of the run.
 struct Cursor {
   long long t, t_lo, t_hi;
-  const long long* pre;
-  int S, Hkv;
   int b, kvh, j, T, e;
   __device__ __forceinline__ bool first() const { return t == t_lo || j == 0; }
   __device__ __forceinline__ bool last() const { return t == t_hi - 1 || j == T - 1; }
   __device__ __forceinline__ bool done() const { return t >= t_hi; }
-  __device__ __forceinline__ void next() {
+  __device__ __forceinline__ void next(const Args& a) {
     ++t;
     if (++j == T) {
       j = 0;
       ++e;
-      if (++kvh == Hkv) {
+      if (++kvh == a.Hkv) {
         kvh = 0;
         if (t < t_hi) {
-          do {
-            ++b;
-            T = static_cast<int>(pre[b + 1] - pre[b]);
-          } while (T == 0);  // ends: tile t < t_hi <= W lies in a later sequence
+          bool bad = false;
+          do T = seq_tiles(a, ++b, bad);
+          while (T == 0);  // ends: tile t < t_hi <= W lies in a later sequence
         }
       }
     }
   }
 };
 
-// Finds the sequence of tile t by a 32-way search of the whole warp: the
-// largest b with Hkv * pre[b] <= t.
-__device__ __forceinline__ int find_seq(const long long* pre, int S, int Hkv, long long t, int lane) {
-  int lo = 0, n = S;
-  while (n > 1) {
-    const int step = (n + 31) / 32;
-    const int k = lane * step;
-    const bool le = k < n && pre[lo + k] * Hkv <= t;
-    const int cnt = __popc(__ballot_sync(0xffffffffu, le));
-    lo += (cnt - 1) * step;
-    n = min(step, n - (cnt - 1) * step);
+__device__ __forceinline__ long long warp_scan(long long x, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
   }
-  return lo;
+  return x;
 }
 
-// Sums the sequences' tiles, T_b = max(1, ceil(len_b / 128)) where there are
-// new tokens, and reports lengths and offsets that are out of range. One
-// block.
-__global__ void __launch_bounds__(1024) paged_few_plan_kernel(const int* cu, const int* lens, int S, int T, int max_q,
-                                                              long long max_len, long long* tile_pre,
-                                                              unsigned int* err) {
-  pdl_launch_dependents();
-  __shared__ long long warp_sum[32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long base = 0;
-  bool bad = false;
-  if (threadIdx.x == 0) tile_pre[0] = 0;
-  for (int b0 = 0; b0 < S; b0 += 1024) {
-    const int b = b0 + threadIdx.x;
-    long long x = 0;
-    if (b < S) {
-      const SeqRange s = seq_range(cu, lens, b, T, max_q, max_len);
-      bad |= s.bad;
-      x = s.n > 0 ? max(1, (s.len + kT - 1) / kT) : 0;
-    }
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    if (lane == 31) warp_sum[warp] = x;
-    __syncthreads();
-    if (warp == 0) {
-      long long y = warp_sum[lane];
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long z = __shfl_up_sync(0xffffffffu, y, o);
-        if (lane >= o) y += z;
-      }
-      warp_sum[lane] = y;
-    }
-    __syncthreads();
-    if (b < S) tile_pre[b + 1] = base + x + (warp ? warp_sum[warp - 1] : 0);
-    base += warp_sum[31];
-    __syncthreads();
+// This CTA's run, by the whole warp. Lane i first sums the tiles of the i-th
+// 32nd of the sequences; the 32nd that holds the run's first tile is then
+// looked through 32 sequences at a time. W: all tiles; 0 (no work at all)
+// where a length or an offset is out of range.
+__device__ __forceinline__ Cursor first_tile(const Args& a, int lane, long long& W, bool& bad) {
+  const int per = (a.S + 31) / 32;
+  long long mine = 0;
+  bad = false;
+  for (int i = 0; i < per; ++i) {
+    const int b = lane * per + i;
+    if (b < a.S) mine += seq_tiles(a, b, bad);
   }
-  // Nothing is computed when a length or an offset is out of range.
-  if (__syncthreads_or(bad)) {
-    if (threadIdx.x == 0) atomicOr(err, kErrData);
-    for (int b = threadIdx.x; b <= S; b += 1024) tile_pre[b] = 0;
+  bad = __any_sync(0xffffffffu, bad);
+  const long long incl = warp_scan(mine, lane);
+  W = bad ? 0 : __shfl_sync(0xffffffffu, incl, 31) * a.Hkv;
+  const int G = runs_of(W, gridDim.x);
+  Cursor c;
+  c.t = c.t_lo = run_lo(min(static_cast<int>(blockIdx.x), G), W, G);
+  c.t_hi = run_lo(min(static_cast<int>(blockIdx.x) + 1, G), W, G);
+  c.b = c.kvh = c.j = c.e = 0;
+  c.T = 1;
+  if (c.done()) return c;
+  // The first lane whose part ends behind the tile.
+  const int part = __ffs(__ballot_sync(0xffffffffu, incl * a.Hkv > c.t)) - 1;
+  long long before = __shfl_sync(0xffffffffu, incl - mine, part);
+  for (int i0 = 0; i0 < per; i0 += 32) {
+    const int b = part * per + i0 + lane;
+    bool unused = false;
+    const int tiles = i0 + lane < per && b < a.S ? seq_tiles(a, b, unused) : 0;
+    const long long in = before + warp_scan(tiles, lane);
+    const unsigned hit = __ballot_sync(0xffffffffu, in * a.Hkv > c.t);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      c.b = part * per + i0 + l;
+      c.T = __shfl_sync(0xffffffffu, tiles, l);
+      const long long in_seq = c.t - (__shfl_sync(0xffffffffu, in, l) - c.T) * a.Hkv;
+      c.kvh = static_cast<int>(static_cast<unsigned long long>(in_seq) / static_cast<unsigned>(c.T));
+      c.j = static_cast<int>(in_seq - static_cast<long long>(c.kvh) * c.T);
+      break;
+    }
+    before = __shfl_sync(0xffffffffu, in, 31);
   }
+  return c;
 }
 
 template <int D, int RHO>
@@ -247,26 +250,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = bars->tmem_base;
   const Watch w{&bars->abort, a.ctl.err, a.ctl.budget_ns};
   pdl_launch_dependents();  // the merge kernel may be scheduled; it waits for this grid's end
-  pdl_wait();               // the plan is written
 
-  const long long W = a.tile_pre[a.S] * a.Hkv;
-  Cursor start;
-  const int G = runs_of(W, gridDim.x);
-  start.t = start.t_lo = run_lo(min(static_cast<int>(blockIdx.x), G), W, G);
-  start.t_hi = run_lo(min(static_cast<int>(blockIdx.x) + 1, G), W, G);
-  start.pre = a.tile_pre;
-  start.S = a.S;
-  start.Hkv = a.Hkv;
-  start.e = 0;
-  start.b = start.kvh = start.j = 0;
-  start.T = 1;
-  if (!start.done()) {
-    start.b = find_seq(a.tile_pre, a.S, a.Hkv, start.t, lane);
-    start.T = static_cast<int>(a.tile_pre[start.b + 1] - a.tile_pre[start.b]);
-    const long long in_seq = start.t - a.tile_pre[start.b] * a.Hkv;
-    start.kvh = static_cast<int>(in_seq / start.T);
-    start.j = static_cast<int>(in_seq - static_cast<long long>(start.kvh) * start.T);
-  }
+  long long W;
+  bool bad;
+  const Cursor start = first_tile(a, lane, W, bad);
   const long long t_lo = start.t_lo;
   auto all = [](bool b) { return __all_sync(0xffffffffu, b); };
 
@@ -281,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int len = 0, tok = 0, last_b = -1;
     int issued = 0, q_issued = 0;
     uint32_t tail_last = 0, land_par = 0;  // per stage: last use was a tail; parity of its next landing phase
-    for (Cursor ta = start; !ta.done(); ta.next()) {
+    for (Cursor ta = start; !ta.done(); ta.next(a)) {
       if (ta.b != last_b) {
         last_b = ta.b;
         len = a.lens[ta.b];
@@ -357,9 +344,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
   } else if (warp == kFixer) {
     // ------------------------------ V rows behind the sequence's last key
+    if (blockIdx.x == 0) {
+      // Also the merge's sums, and what there is to report.
+      if (bad && lane == 0) atomicOr(a.ctl.err, kErrData);
+      long long before = 0;
+      for (int b0 = 0; b0 < a.S; b0 += 32) {
+        bool unused = false;
+        const long long x = before + warp_scan(b0 + lane < a.S && !bad ? seq_tiles(a, b0 + lane, unused) : 0, lane);
+        if (b0 + lane < a.S) a.tile_pre[b0 + lane + 1] = x;
+        before = __shfl_sync(0xffffffffu, x, 31);
+      }
+      if (lane == 0) a.tile_pre[0] = 0;
+    }
     int len = 0, last_b = -1;
     uint32_t land_par = 0;
-    for (Cursor ta = start; !ta.done(); ta.next()) {
+    for (Cursor ta = start; !ta.done(); ta.next(a)) {
       if (ta.b != last_b) {
         last_b = ta.b;
         len = a.lens[ta.b];
@@ -433,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       Cursor cur = start, nxt = start;
       bool ok = issue_s(nxt);
-      for (nxt.next(); ok && !cur.done(); cur.next(), nxt.next()) {
+      for (nxt.next(a); ok && !cur.done(); cur.next(a), nxt.next(a)) {
         const bool more = !nxt.done();
         // With one Q buffer the next segment's Q lands only after this
         // segment's last S: hand P_t V_t to the tensor pipe before waiting.
@@ -468,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float l = 0.f;
     int lim = 0, last_b = -1;  // last visible key
     bool valid = false;
-    for (Cursor ta = start; !ta.done(); ta.next()) {
+    for (Cursor ta = start; !ta.done(); ta.next(a)) {
       const int g = static_cast<int>(ta.t - t_lo);
       const bool first = ta.first();
       const int ob = ta.e % OB;
@@ -628,80 +627,78 @@ __device__ __forceinline__ void load_vec(const float* p, float (&x)[2]) {
 }
 
 // Merges the partials of a unit's rows (every copy of every segment), one
-// warp per row; grid (S * Hkv, groups of four rows). Lanes first take one
-// partial each for the max and the sum of e^(L_s - max); the weighted sum of
-// the partial O rows then runs over d across lanes, eight partials a step so
-// that their loads overlap.
+// warp per row; grid (S * Hkv, groups of four rows). 32 partials a step: each
+// lane takes one logsumexp, whose max and sum go through the warp; the
+// weighted sum of the partial O rows runs over d across lanes, eight partials
+// at a time so that their loads overlap.
 template <int D>
 __global__ void __launch_bounds__(128)
-    paged_few_merge_kernel(const Args a, int ctas, int rho, Rows o, float* __restrict__ lse, int T) {
-  pdl_wait();
+    paged_few_merge_kernel(const Args a, int ctas, int rho, Rows o, float* __restrict__ lse) {
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int b = blockIdx.x / a.Hkv;
   const int kvh = blockIdx.x - b * a.Hkv;
+  const int rr = blockIdx.y * 4 + warp;
+  const int tok0 = a.cu ? a.cu[b] : b;
+  const int n = a.cu ? a.cu[b + 1] - tok0 : 1;
+  pdl_wait();
   const long long pre = a.tile_pre[b];
   const int Tb = static_cast<int>(a.tile_pre[b + 1] - pre);
   const long long W = a.tile_pre[a.S] * a.Hkv;
-  const int G = runs_of(W, ctas);
-  const int tok0 = a.cu ? a.cu[b] : b;
-  const int n = a.cu ? a.cu[b + 1] - tok0 : 1;
-  const int rr = blockIdx.y * 4 + warp;
   if (Tb == 0 || rr >= n * a.r) return;
+  const int G = runs_of(W, ctas);
   const long long first = pre * a.Hkv + static_cast<long long>(kvh) * Tb;
   const int c0 = run_of(first, W, G);
   const int n_parts = (run_of(first + Tb - 1, W, G) - c0 + 1) * rho;
   // Partial p = (run c0 + p / rho, copy p % rho).
   const long long base = (static_cast<long long>(blockIdx.x) + c0) * rho;
   auto prow_of = [&](int p) -> long long { return (base + p) * a.rv + rr; };
-  float mx = -CUDART_INF_F;
-  for (int p = lane; p < n_parts; p += 32) mx = fmaxf(mx, a.part_l[prow_of(p)]);
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-  float den = 0.f;
-  const float mz = mx == -CUDART_INF_F ? 0.f : mx;  // no key at all: every weight 0
-  for (int p = lane; p < n_parts; p += 32) den += expf(a.part_l[prow_of(p)] - mz);
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) den += __shfl_xor_sync(0xffffffffu, den, off);
-  const float L = mz + logf(den);
-  const float Lz = den == 0.f ? 0.f : L;
   constexpr int VW = D / 32;
-  float acc[VW];
+  float acc[VW], m = -CUDART_INF_F, den = 0.f;
 #pragma unroll
   for (int i = 0; i < VW; ++i) acc[i] = 0.f;
   for (int p0 = 0; p0 < n_parts; p0 += 32) {
-    const int p = p0 + lane;
-    float wl = 0.f;
-    if (p < n_parts) wl = expf(a.part_l[prow_of(p)] - Lz);
     const int cnt = min(32, n_parts - p0);
+    const float pl = lane < cnt ? a.part_l[prow_of(p0 + lane)] : -CUDART_INF_F;
+    float top = pl;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    top = fmaxf(top, m);
+    const float ref = top == -CUDART_INF_F ? 0.f : top;  // no key so far: every weight 0
+    const float old = expf(m - ref);
+    const float wl = expf(pl - ref);
+    float sum = wl;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    den = den * old + sum;
+    m = top;
+#pragma unroll
+    for (int k = 0; k < VW; ++k) acc[k] *= old;
     for (int i = 0; i < cnt; i += 8) {
-      float wv[8], x[8][VW];
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        wv[q] = __shfl_sync(0xffffffffu, wl, (i + q) & 31);
-        if (i + q < cnt && wv[q] != 0.f) {
-          load_vec(a.part_o + prow_of(p0 + i + q) * D + lane * VW, x[q]);
-        } else {
-          wv[q] = 0.f;
-#pragma unroll
-          for (int k = 0; k < VW; ++k) x[q][k] = 0.f;
-        }
-      }
+      float x[8][VW];
 #pragma unroll
       for (int q = 0; q < 8; ++q)
+        if (i + q < cnt) load_vec(a.part_o + prow_of(p0 + i + q) * D + lane * VW, x[q]);
 #pragma unroll
-        for (int k = 0; k < VW; ++k) acc[k] = fmaf(wv[q], x[q][k], acc[k]);
+      for (int q = 0; q < 8; ++q) {
+        const float wq = __shfl_sync(0xffffffffu, wl, (i + q) & 31);
+        if (i + q < cnt && wq != 0.f)
+#pragma unroll
+          for (int k = 0; k < VW; ++k) acc[k] = fmaf(wq, x[q][k], acc[k]);
+      }
     }
   }
+  const float inv = den == 0.f ? 0.f : 1.f / den;
   const int tok = tok0 + rr / a.r;
   const int h = kvh * a.r + rr % a.r;
   __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(o.p) + tok * o.ts + h * o.hs + lane * VW;
   if constexpr (VW == 4) {
-    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]));
+    *reinterpret_cast<uint2*>(dst) =
+        make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
   } else {
-    *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0], acc[1]);
+    *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
   }
-  if (lane == 0) lse[static_cast<long long>(h) * T + tok] = L;
+  if (lane == 0) lse[static_cast<long long>(h) * a.T + tok] = den == 0.f ? -CUDART_INF_F : m + logf(den);
 }
 
 struct Plan {
@@ -727,21 +724,6 @@ Plan make_plan(const SeqShape& s, const CacheShape& c, int ctas) {
   return p;
 }
 
-template <typename... P, typename... A>
-cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
-}
-
 template <int D, int RHO>
 cudaError_t launch_t(const SeqShape& s, const CacheShape& c, const Plan& p, const CUtensorMap& tq,
                      const CUtensorMap& tk, const CUtensorMap& tv, const Rows& o, float* lse, void* workspace,
@@ -754,13 +736,15 @@ cudaError_t launch_t(const SeqShape& s, const CacheShape& c, const Plan& p, cons
   Args a;
   a.part_o = reinterpret_cast<float*>(ws);
   a.part_l = reinterpret_cast<float*>(ws + p.off_l);
-  long long* pre = reinterpret_cast<long long*>(ws + p.off_pre);
-  a.tile_pre = pre;
+  a.tile_pre = reinterpret_cast<long long*>(ws + p.off_pre);
   a.cu = s.cu;
   a.lens = c.lens;
   a.table = c.table;
   a.table_stride = c.table_stride;
+  a.max_len = static_cast<long long>(c.max_pages) * c.page;
   a.S = s.S;
+  a.T = s.T;
+  a.max_q = c.max_q;
   a.Hkv = s.Hkv;
   a.r = s.r();
   a.n_pages = c.n_pages;
@@ -771,13 +755,10 @@ cudaError_t launch_t(const SeqShape& s, const CacheShape& c, const Plan& p, cons
   a.q_tokens = p.q_tokens;
   a.scale_log2 = s.scale * 1.4426950408889634f;
   a.ctl = ctl;
-  paged_few_plan_kernel<<<1, 1024, 0, stream>>>(s.cu, c.lens, s.S, s.T, c.max_q,
-                                                static_cast<long long>(c.max_pages) * c.page, pre, ctl.err);
+  kern<<<p.G, kThreads, C::kSmemBytes, stream>>>(tq, tk, tv, a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  e = launch_dependent(kern, dim3(p.G), kThreads, C::kSmemBytes, stream, tq, tk, tv, a);
-  if (e != cudaSuccess) return e;
   return launch_dependent(paged_few_merge_kernel<D>, dim3(s.S * s.Hkv, (p.rv + 3) / 4), 128, 0, stream, a, p.G, RHO,
-                          o, lse, s.T);
+                          o, lse);
 }
 
 }  // namespace
