@@ -1,4 +1,5 @@
-"""ctypes binding of libfa.so (include/fa.h): argument marshalling only.
+"""Binding of libfa.so (include/fa.h): argument marshalling only, by ctypes or, for the packed, paged and rotary
+calls, by the native module ``_fa_torch``.
 
 Each function takes torch CUDA tensors, checks that they have the layout the
 C ABI documents, and passes raw device pointers, sizes and the current CUDA
@@ -9,7 +10,6 @@ no CPU fallback, and a missing library or device raises ``RuntimeError``.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 
 import torch
@@ -117,8 +117,7 @@ def status_string(status: int) -> str:
 
 def _stream(stream) -> int:
     if stream is None:
-        # The current stream's handle, without building a Stream object (3 us).
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -282,76 +281,31 @@ def fa_decode(q, k, v, o, lse, causal: bool, scale: float, workspace, stream=Non
 
 
 # ------------------------------------------ packed sequences, paged cache
+#
+# These calls go through the native binding (csrc/torch_binding.cpp): checks, views, allocation and the call itself.
 
-def _check_view(name, t, dtype, shape, dev):
-    """A CUDA tensor of this type and shape on device ``dev`` whose last dimension is contiguous; its strides."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise RuntimeError(f"{name} must be a CUDA tensor (there is no CPU path)")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on cuda:{t.get_device()} but the current device is cuda:{dev}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    st = t.stride()
-    if st[-1] != 1 and shape[-1] > 1:
-        raise ValueError(f"{name} must be contiguous in its last dimension")
-    return st
+_native = None
 
 
-def _rows(name, t, shape, dev):
-    """``fa_rows`` of a bf16 [T, H, d] view. (The usual case is looked at first: a call marshals up to nine.)"""
-    if not (isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.get_device() == dev and t.shape == shape):
-        _check_view(name, t, torch.bfloat16, shape, dev)
-    ts, hs, ds = t.stride()
-    if ds != 1:
-        _check_view(name, t, torch.bfloat16, shape, dev)
-    return Rows(t.data_ptr(), ts, hs)
+def _binding():
+    """The native binding of libfa.so; raises if it has not been built."""
+    global _native
+    if _native is None:
+        lib()
+        try:
+            from . import _fa_torch
+        except ImportError as e:
+            raise RuntimeError("the torch binding is missing: build it with `python -m exact_io_aware_56_b200.build`") from e
+        _fa_torch.set_error(FaError)
+        _native = _fa_torch
+    return _native
 
 
-def _pages(name, t, shape, dev):
-    st = _check_view(name, t, torch.bfloat16, shape, dev)
-    return Pages(t.data_ptr(), st[0], st[1], st[2])
-
-
-def _flat(name, t, dtype, shape, dev):
-    """Address of a contiguous tensor (``None`` for ``None``)."""
-    if t is None:
+def _handle(stream):
+    """Stream handle for the binding; ``None`` (the current stream) stays ``None``."""
+    if stream is None:
         return None
-    _check_view(name, t, dtype, shape, dev)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
-
-
-def _workspace(t, dev):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or not t.is_contiguous():
-        raise ValueError("workspace must be a contiguous CUDA tensor")
-    if t.get_device() != dev:
-        raise ValueError(f"workspace is on cuda:{t.get_device()} but the current device is cuda:{dev}")
-    return t.data_ptr(), t.numel() * t.element_size()
-
-
-def _three(name, t):
-    if not isinstance(t, torch.Tensor) or t.dim() != 3:
-        raise ValueError(f"{name} must be a [T, H, d] tensor")
-    return t.shape
-
-
-def _seqs(cu_seqlens, T, dev):
-    """(S, address) of the offsets; ``None``: one token per sequence."""
-    if cu_seqlens is None:
-        return T, None
-    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
-        raise ValueError("cu_seqlens must be a tensor of S + 1 offsets")
-    return cu_seqlens.numel() - 1, _flat("cu_seqlens", cu_seqlens, torch.int32, cu_seqlens.shape, dev)
-
-
-def _ok(rc, where):
-    if rc != FA_OK:
-        raise FaError(rc, where)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def fa_packed_fwd_workspace_bytes(S: int, T: int, Hq: int, Hkv: int, d: int) -> int:
@@ -363,19 +317,7 @@ def fa_packed_fwd(q, k, v, o, lse, cu_seqlens, causal: bool, scale: float, works
     """Forward over packed sequences: ``q``, ``o`` (and ``o_resid``) [T,Hq,d], ``k``, ``v`` [T,Hkv,d] bf16 views,
     ``lse`` [Hq,T] fp32, ``cu_seqlens`` int32 [S+1]; ``workspace`` a uint8 CUDA tensor of at least
     :func:`fa_packed_fwd_workspace_bytes` bytes."""
-    dev = torch.cuda.current_device()
-    sq, sk = _three("q", q), _three("k", k)
-    T, Hq, d = sq
-    sk = torch.Size((T, sk[1], d))
-    S, cu = _seqs(cu_seqlens, T, dev)
-    if cu is None:
-        raise ValueError("cu_seqlens is required")
-    args = [_rows("q", q, sq, dev), _rows("k", k, sk, dev), _rows("v", v, sk, dev), _rows("o", o, sq, dev),
-            None if o_resid is None else _rows("o_resid", o_resid, sq, dev)]
-    la = _flat("lse", lse, torch.float32, (Hq, T), dev)
-    wa, wb = _workspace(workspace, dev)
-    _ok(lib().fa_packed_fwd(*args, la, cu, S, T, Hq, sk[1], d, int(bool(causal)), float(scale), wa, wb,
-                            _stream(stream)), "fa_packed_fwd")
+    _binding().packed_fwd(q, k, v, o, lse, o_resid, False, cu_seqlens, bool(causal), scale, workspace, _handle(stream))
 
 
 def fa_packed_bwd_workspace_bytes(S: int, T: int, Hq: int, Hkv: int, d: int) -> int:
@@ -385,34 +327,8 @@ def fa_packed_bwd_workspace_bytes(S: int, T: int, Hq: int, Hkv: int, d: int) -> 
 def fa_packed_bwd(q, k, v, o, dout, lse, dq, dk, dv, cu_seqlens, causal: bool, scale: float, workspace, stream=None,
                   o_resid=None) -> None:
     """Backward of :func:`fa_packed_fwd` into ``dq`` [T,Hq,d], ``dk``, ``dv`` [T,Hkv,d]."""
-    dev = torch.cuda.current_device()
-    sq, sk = _three("q", q), _three("k", k)
-    T, Hq, d = sq
-    sk = torch.Size((T, sk[1], d))
-    S, cu = _seqs(cu_seqlens, T, dev)
-    if cu is None:
-        raise ValueError("cu_seqlens is required")
-    ins = [_rows("q", q, sq, dev), _rows("k", k, sk, dev), _rows("v", v, sk, dev), _rows("o", o, sq, dev),
-           None if o_resid is None else _rows("o_resid", o_resid, sq, dev), _rows("dout", dout, sq, dev)]
-    la = _flat("lse", lse, torch.float32, (Hq, T), dev)
-    outs = [_rows("dq", dq, sq, dev), _rows("dk", dk, sk, dev), _rows("dv", dv, sk, dev)]
-    wa, wb = _workspace(workspace, dev)
-    _ok(lib().fa_packed_bwd(*ins, la, *outs, cu, S, T, Hq, sk[1], d, int(bool(causal)), float(scale), wa, wb,
-                            _stream(stream)), "fa_packed_bwd")
-
-
-def _cache(k_pages, v_pages, block_table, seq_lens, S, Hkv, d, dev):
-    if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
-        raise ValueError("k_pages must be [n_pages, Hkv, page_size, d]")
-    shape = torch.Size((k_pages.shape[0], Hkv, k_pages.shape[2], d))
-    kp, vp = _pages("k_pages", k_pages, shape, dev), _pages("v_pages", v_pages, shape, dev)
-    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
-        raise ValueError("block_table must be [S, max_pages]")
-    bt = _check_view("block_table", block_table, torch.int32, (S, block_table.shape[1]), dev)
-    ln = _flat("seq_lens", seq_lens, torch.int32, (S,), dev)
-    if ln is None:
-        raise ValueError("seq_lens is required")
-    return kp, vp, shape[0], shape[2], block_table.data_ptr(), bt[0], block_table.shape[1], ln
+    _binding().packed_bwd(q, k, v, o, o_resid, dout, lse, dq, dk, dv, cu_seqlens, bool(causal), scale, workspace,
+                          _handle(stream))
 
 
 def fa_paged_fwd_workspace_bytes(S: int, T: int, max_q: int, Hq: int, Hkv: int, d: int, page_size: int,
@@ -426,35 +342,8 @@ def fa_paged_fwd(q, k_pages, v_pages, o, lse, block_table, seq_lens, cu_seqlens,
     [n_pages,Hkv,page_size,d] into ``o`` [T,Hq,d] and ``lse`` [Hq,T]; ``block_table`` int32 [S,max_pages],
     ``seq_lens`` int32 [S] (new tokens counted), ``cu_seqlens`` int32 [S+1] or ``None`` (one token each), no
     sequence with more than ``max_q`` new tokens."""
-    dev = torch.cuda.current_device()
-    sq = _three("q", q)
-    T, Hq, d = sq
-    S, cu = _seqs(cu_seqlens, T, dev)
-    Hkv = k_pages.shape[1] if isinstance(k_pages, torch.Tensor) and k_pages.dim() == 4 else 0
-    kp, vp, n_pages, page, bt, bts, max_pages, ln = _cache(k_pages, v_pages, block_table, seq_lens, S, Hkv, d, dev)
-    qa, oa = _rows("q", q, sq, dev), _rows("o", o, sq, dev)
-    la = _flat("lse", lse, torch.float32, (Hq, T), dev)
-    wa, wb = _workspace(workspace, dev)
-    _ok(lib().fa_paged_fwd(qa, kp, vp, oa, la, n_pages, page, bt, bts, max_pages, ln, cu, S, T, int(max_q), Hq, Hkv, d,
-                           int(bool(causal)), float(scale), wa, wb, _stream(stream)), "fa_paged_fwd")
-
-
-@functools.lru_cache(maxsize=64)
-def _section_array(sections):
-    return (ctypes.c_int * len(sections))(*sections)
-
-
-def _sections(sections, inv_freq):
-    """(sections, their C array, pairs)."""
-    if inv_freq is None:
-        if sections is not None and len(sections):
-            raise ValueError("sections need inv_freq")
-        return 0, None, 0
-    pairs = inv_freq.numel()
-    sections = (pairs,) if sections is None else tuple(map(int, sections))
-    if sum(sections) != pairs:
-        raise ValueError(f"sections {sections} must sum to inv_freq's {pairs} pairs")
-    return len(sections), _section_array(sections), pairs
+    _binding().paged_fwd(q, k_pages, v_pages, o, lse, block_table, seq_lens, cu_seqlens, max_q, bool(causal), scale,
+                         workspace, _handle(stream))
 
 
 def fa_rope(q, k, q_out, k_out, positions, inv_freq, sections=None, interleaved: bool = False, inverse: bool = False,
@@ -462,21 +351,7 @@ def fa_rope(q, k, q_out, k_out, positions, inv_freq, sections=None, interleaved:
     """Rotary positions of ``q`` [T,Hq,d] and ``k`` [T,Hkv,d] (either may be ``None``) into ``q_out``, ``k_out``
     (which may be ``q``, ``k``): ``positions`` int32 [axes,T], ``inv_freq`` float64 [pairs], ``sections`` the pairs
     of each axis (default: all of axis 0)."""
-    dev = torch.cuda.current_device()
-    if q is None and k is None:
-        raise ValueError("q or k is required")
-    T, _, d = _three("q" if q is not None else "k", q if q is not None else k)
-    sq = torch.Size((T, 0, d)) if q is None else _three("q", q)
-    sk = torch.Size((T, 0, d)) if k is None else torch.Size((T, _three("k", k)[1], d))
-    if inv_freq is None or positions is None:
-        raise ValueError("positions and inv_freq are required")
-    n, sec, pairs = _sections(sections, inv_freq)
-    fa_ = _flat("inv_freq", inv_freq, torch.float64, (pairs,), dev)
-    pa = _flat("positions", positions, torch.int32, (n, T), dev)
-    args = [None if q is None else _rows("q", q, sq, dev), None if k is None else _rows("k", k, sk, dev),
-            None if q is None else _rows("q_out", q_out, sq, dev), None if k is None else _rows("k_out", k_out, sk, dev)]
-    _ok(lib().fa_rope(*args, pa, fa_, sec, n, T, sq[1], sk[1], d, int(bool(interleaved)), int(bool(inverse)),
-                      _stream(stream)), "fa_rope")
+    _binding().rope(q, k, q_out, k_out, positions, inv_freq, sections, bool(interleaved), bool(inverse), _handle(stream))
 
 
 def fa_paged_append(q, k, v, q_out, k_pages, v_pages, block_table, seq_lens, cu_seqlens, positions=None, inv_freq=None,
@@ -484,19 +359,8 @@ def fa_paged_append(q, k, v, q_out, k_pages, v_pages, block_table, seq_lens, cu_
     """Appends ``k``, ``v`` [T,Hkv,d] of the new tokens to the paged cache, in place; with ``inv_freq`` the keys are
     turned first, and ``q`` [T,Hq,d] (or ``None``) into ``q_out``, by ``positions`` int32 [axes,T] (``None``: the
     places in the cache). Cache arguments as :func:`fa_paged_fwd`."""
-    dev = torch.cuda.current_device()
-    sk = _three("k", k)
-    T, Hkv, d = sk
-    sq = torch.Size((T, 0, d)) if q is None else torch.Size((T, _three("q", q)[1], d))
-    S, cu = _seqs(cu_seqlens, T, dev)
-    kp, vp, n_pages, page, bt, bts, max_pages, ln = _cache(k_pages, v_pages, block_table, seq_lens, S, Hkv, d, dev)
-    n, sec, pairs = _sections(sections, inv_freq)
-    fa_ = _flat("inv_freq", inv_freq, torch.float64, (pairs,), dev)
-    pa = _flat("positions", positions, torch.int32, (n, T), dev)
-    args = [None if q is None else _rows("q", q, sq, dev), _rows("k", k, sk, dev), _rows("v", v, sk, dev),
-            None if q is None else _rows("q_out", q_out, sq, dev)]
-    _ok(lib().fa_paged_append(*args, kp, vp, n_pages, page, bt, bts, max_pages, ln, cu, S, T, pa, fa_, sec, n, sq[1],
-                              Hkv, d, int(bool(interleaved)), _stream(stream)), "fa_paged_append")
+    _binding().paged_append(q, k, v, q_out, k_pages, v_pages, block_table, seq_lens, cu_seqlens, positions, inv_freq,
+                            sections, bool(interleaved), _handle(stream))
 
 
 def fa_check_device_error(stream=None) -> int:
@@ -595,28 +459,6 @@ def attention_forward_fp8(q, k, v, causal: bool, scale: float | None = None, str
     return o, lse, (q8, sq, k8, sk, v8, sv)
 
 
-def _side_stream(stream, *inputs):
-    """For a call on a stream other than the current one: that stream, after telling the caching allocator that the
-    inputs are used on it; else ``None``."""
-    if stream is None:
-        return None
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream))
-    if s == torch.cuda.current_stream():
-        return None
-    for t in inputs:
-        if isinstance(t, torch.Tensor) and t.is_cuda:
-            t.record_stream(s)
-    return s
-
-
-def _empty(like, shape, dtype=None, side=None):
-    """New contiguous memory, on a side stream where there is one, so that it belongs to that stream."""
-    if side is None:
-        return like.new_empty(shape, dtype=dtype)
-    with torch.cuda.stream(side):
-        return like.new_empty(shape, dtype=dtype)
-
-
 def attention_packed_forward(q, k, v, cu_seqlens, causal: bool, scale: float | None = None, stream=None,
                              residual: bool = False, workspace=None):
     """Allocates the outputs (and the workspace if not given) and runs :func:`fa_packed_fwd`.
@@ -624,34 +466,15 @@ def attention_packed_forward(q, k, v, cu_seqlens, causal: bool, scale: float | N
     Returns ``(o, lse)``, or ``(o, lse, o_resid)`` when ``residual`` is true. Rows outside every sequence are not
     written.
     """
-    T, Hq, d = _three("q", q)
-    scale = d ** -0.5 if scale is None else scale
-    side = _side_stream(stream, q, k, v, cu_seqlens, workspace)
-    if workspace is None:
-        need = fa_packed_fwd_workspace_bytes(cu_seqlens.numel() - 1, T, Hq, _three("k", k)[1], d)
-        workspace = _empty(q, max(16, need), torch.uint8, side)
-    o = _empty(q, (T, Hq, d), None, side)
-    lse = _empty(q, (Hq, T), torch.float32, side)
-    o_resid = _empty(q, (T, Hq, d), None, side) if residual else None
-    fa_packed_fwd(q, k, v, o, lse, cu_seqlens, causal, scale, workspace, stream, o_resid=o_resid)
-    return (o, lse, o_resid) if residual else (o, lse)
+    return _binding().packed_fwd(q, k, v, None, None, None, bool(residual), cu_seqlens, bool(causal), scale, workspace,
+                                 _handle(stream))
 
 
 def attention_packed_backward(q, k, v, o, dout, lse, cu_seqlens, causal: bool, scale: float | None = None,
                               workspace=None, stream=None, o_resid=None):
     """Allocates ``dq``, ``dk``, ``dv`` (and the workspace if not given) and runs :func:`fa_packed_bwd`."""
-    T, Hq, d = _three("q", q)
-    Hkv = _three("k", k)[1]
-    scale = d ** -0.5 if scale is None else scale
-    side = _side_stream(stream, q, k, v, o, dout, lse, cu_seqlens, o_resid, workspace)
-    if workspace is None:
-        need = fa_packed_bwd_workspace_bytes(cu_seqlens.numel() - 1, T, Hq, Hkv, d)
-        workspace = _empty(q, max(16, need), torch.uint8, side)
-    dq = _empty(q, (T, Hq, d), None, side)
-    dk = _empty(q, (T, Hkv, d), None, side)
-    dv = _empty(q, (T, Hkv, d), None, side)
-    fa_packed_bwd(q, k, v, o, dout, lse, dq, dk, dv, cu_seqlens, causal, scale, workspace, stream, o_resid=o_resid)
-    return dq, dk, dv
+    return _binding().packed_bwd(q, k, v, o, o_resid, dout, lse, None, None, None, cu_seqlens, bool(causal), scale,
+                                 workspace, _handle(stream))
 
 
 def attention_paged(q, k_pages, v_pages, block_table, seq_lens, cu_seqlens=None, max_q: int | None = None,
@@ -661,35 +484,18 @@ def attention_paged(q, k_pages, v_pages, block_table, seq_lens, cu_seqlens=None,
     ``cu_seqlens`` ``None``: one new token per sequence. ``max_q`` defaults to 1 then, and otherwise to T (a tight
     bound picks the faster kernel and needs less workspace). Returns ``(o, lse)``.
     """
-    T, Hq, d = _three("q", q)
-    scale = d ** -0.5 if scale is None else scale
-    if max_q is None:
-        max_q = 1 if cu_seqlens is None else max(1, T)
-    side = _side_stream(stream, q, k_pages, v_pages, block_table, seq_lens, cu_seqlens, workspace)
-    if workspace is None:
-        S = T if cu_seqlens is None else cu_seqlens.numel() - 1
-        need = fa_paged_fwd_workspace_bytes(S, T, max_q, Hq, k_pages.shape[1], d, k_pages.shape[2], block_table.shape[1])
-        workspace = _empty(q, max(16, need), torch.uint8, side)
-    o = _empty(q, (T, Hq, d), None, side)
-    lse = _empty(q, (Hq, T), torch.float32, side)
-    fa_paged_fwd(q, k_pages, v_pages, o, lse, block_table, seq_lens, cu_seqlens, max_q, causal, scale, workspace, stream)
-    return o, lse
+    return _binding().paged_fwd(q, k_pages, v_pages, None, None, block_table, seq_lens, cu_seqlens, max_q, bool(causal),
+                                scale, workspace, _handle(stream))
 
 
 def paged_append(k, v, k_pages, v_pages, block_table, seq_lens, cu_seqlens=None, q=None, positions=None, inv_freq=None,
                  sections=None, interleaved: bool = False, stream=None):
     """Runs :func:`fa_paged_append`; returns the (turned) ``q`` in a new tensor, or ``None`` without ``q``."""
-    side = _side_stream(stream, q, k, v, k_pages, v_pages, block_table, seq_lens, cu_seqlens, positions, inv_freq)
-    q_out = None if q is None else _empty(q, _three("q", q), None, side)
-    fa_paged_append(q, k, v, q_out, k_pages, v_pages, block_table, seq_lens, cu_seqlens, positions, inv_freq, sections,
-                    interleaved, stream)
-    return q_out
+    return _binding().paged_append(q, k, v, None, k_pages, v_pages, block_table, seq_lens, cu_seqlens, positions,
+                                   inv_freq, sections, bool(interleaved), _handle(stream))
 
 
 def rope(q, k, positions, inv_freq, sections=None, interleaved: bool = False, inverse: bool = False, stream=None):
     """Allocates the outputs and runs :func:`fa_rope`; returns ``(q_out, k_out)`` (``None`` for ``None``)."""
-    side = _side_stream(stream, q, k, positions, inv_freq)
-    q_out = None if q is None else _empty(q, _three("q", q), None, side)
-    k_out = None if k is None else _empty(k, _three("k", k), None, side)
-    fa_rope(q, k, q_out, k_out, positions, inv_freq, sections, interleaved, inverse, stream)
-    return q_out, k_out
+    return _binding().rope(q, k, None, None, positions, inv_freq, sections, bool(interleaved), bool(inverse),
+                           _handle(stream))

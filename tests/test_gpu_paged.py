@@ -263,3 +263,31 @@ def test_results_repeat(d):
         first = first or got
         assert torch.equal(got[0], first[0]) and torch.equal(got[1], first[1])
     done()
+
+
+def test_binding_refusals():
+    cache = Cache(95, [40], 16, 2, 64)
+    kp, vp, table, ln = cache.cuda()
+    q = normal(96, 1, 4, 64).cuda()
+    ok = dict(k_pages=kp, v_pages=vp, block_table=table, seq_lens=ln)
+
+    def call(q=q, **kw):
+        a = dict(ok, **kw)
+        return fa.attention_paged(q, a.pop("k_pages"), a.pop("v_pages"), a.pop("block_table"), a.pop("seq_lens"), **a)
+
+    call()
+    for kw, err in ((dict(q=q.float()), TypeError), (dict(q=q[..., ::2]), ValueError), (dict(q=q[0]), ValueError),
+                    (dict(k_pages=kp[0]), ValueError), (dict(v_pages=vp[:, :1]), ValueError),
+                    (dict(block_table=table.long()), TypeError), (dict(block_table=table[0]), ValueError),
+                    (dict(seq_lens=ln.repeat(2)), ValueError), (dict(seq_lens=ln.cpu()), RuntimeError),
+                    (dict(cu_seqlens=torch.tensor([0, 1], device="cuda")), TypeError),
+                    (dict(workspace=torch.empty(16, dtype=torch.uint8, device="cuda")), fa.FaError),
+                    (dict(scale=float("nan")), fa.FaError), (dict(max_q=-1), fa.FaError),
+                    (dict(q=normal(1, 1, 3, 64).cuda()), fa.FaError),
+                    (dict(k_pages=kp[:, :, :12], v_pages=vp[:, :, :12]), fa.FaError)):
+        with pytest.raises(err):
+            call(**kw)
+    with pytest.raises(fa.FaError) as e:
+        call(max_q=0)
+    assert e.value.status == fa.FA_ERR_INVALID_ARGUMENT and "fa_paged_fwd" in str(e.value)
+    done()

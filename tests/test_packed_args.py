@@ -3,6 +3,7 @@
 import ctypes
 
 import pytest
+import torch
 
 from exact_io_aware_56_b200 import fa
 
@@ -109,10 +110,21 @@ def test_workspaces():
     assert 0 < one < four
 
 
-def test_binding_checks_before_the_library():
-    torch = pytest.importorskip("torch")
-    if torch.cuda.is_available():
-        pytest.skip("CPU tensors are refused the same way; the rest needs no device")
+def test_binding_refuses_cpu_tensors_and_wrong_types():
     x = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
-    with pytest.raises((RuntimeError, AssertionError)):
+    i = torch.zeros(1, 4, dtype=torch.int32)
+    f = torch.zeros(32, dtype=torch.float64)
+    with pytest.raises(RuntimeError, match="CUDA tensor"):
         fa.attention_packed_forward(x, x, x, torch.tensor([0, 4], dtype=torch.int32), True)
+    with pytest.raises(RuntimeError, match="CUDA tensor"):
+        fa.attention_packed_backward(x, x, x, x, x, x, torch.tensor([0, 4], dtype=torch.int32), True)
+    with pytest.raises(RuntimeError, match="CUDA tensor"):
+        fa.attention_paged(x, x[None], x[None], i, i)
+    with pytest.raises(RuntimeError, match="CUDA tensor"):
+        fa.paged_append(x, x, x[None], x[None], i, i)
+    with pytest.raises(RuntimeError, match="CUDA tensor"):
+        fa.rope(x, x, i, f)
+    with pytest.raises(ValueError, match="required"):
+        fa.rope(None, None, i, f)
+    with pytest.raises(TypeError):
+        fa.rope("q", x, i, f)
