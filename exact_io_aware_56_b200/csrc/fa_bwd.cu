@@ -834,37 +834,58 @@ cudaError_t launch_bwd_t(const AttnShape& s, const CUtensorMap& tq, const CUtens
   return cudaGetLastError();
 }
 
-// D_i and the zeroed dQ accumulator of packed rows: one warp per (head, row),
-// rows outside [cu[0], cu[S]) left out. dsum and dq_acc are [Hq][T] and
-// [Hq][T][D]. Block 0 lists the main kernel's work meanwhile.
+// D_i and the zeroed dQ accumulator of packed rows; rows outside
+// [cu[0], cu[S]) are left out. dsum and dq_acc are [Hq][T] and [Hq][T][D].
+// D / 8 lanes per row, 16 bytes each, so that a token's heads are read in
+// whole lines where they are neighbours in memory; a block takes a token (or
+// several of few heads) at a time. Block 0 lists the main kernel's work
+// meanwhile.
+constexpr int kRowThreads = 256;
+
+// This thread's token within a block's group of `tpb` tokens and its first
+// piece of 16 bytes; `step` pieces further to the next.
+struct RowPieces {
+  int tpb, sub, first, step;
+  __device__ __forceinline__ RowPieces(int items) {
+    tpb = items < kRowThreads ? kRowThreads / items : 1;
+    step = items < kRowThreads ? items : kRowThreads;
+    sub = threadIdx.x / step;
+    first = threadIdx.x - sub * step;
+  }
+};
+
 template <int D>
-__global__ void __launch_bounds__(256) packed_pre_kernel(const PlanArgs plan, Rows o, Rows resid, Rows dout, float* __restrict__ dsum,
-                                                         float* __restrict__ dq_acc, const int* __restrict__ cu, int S,
-                                                         int T, int Hq) {
+__global__ void __launch_bounds__(kRowThreads)
+    packed_pre_kernel(const PlanArgs plan, Rows o, Rows resid, Rows dout, float* __restrict__ dsum,
+                      float* __restrict__ dq_acc, const int* __restrict__ cu, int S, int T, int Hq) {
   if (blockIdx.x == 0) {
     __shared__ PlanShared sh;
-    plan_block<256>(plan, sh);
+    plan_block<kRowThreads>(plan, sh);
     return;
   }
+  constexpr int P = D / 8;  // lanes per row
   const int t0 = max(0, cu[0]), t1 = min(T, cu[S]);
-  const long long warp_g = (static_cast<long long>(blockIdx.x - 1) * blockDim.x + threadIdx.x) >> 5;
-  const int lane = threadIdx.x & 31;
-  const long long nwarps = (static_cast<long long>(gridDim.x - 1) * blockDim.x) >> 5;
-  for (long long e = warp_g; e < static_cast<long long>(T) * Hq; e += nwarps) {
-    const int t = static_cast<int>(e / Hq), h = static_cast<int>(e % Hq);  // heads of a token are neighbours in memory
-    if (t < t0 || t >= t1) continue;
-    const long long row = static_cast<long long>(h) * T + t;
-    auto piece = [&](const Rows& x) {
-      return reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(x.p) + t * x.ts + h * x.hs)[lane];
-    };
-    float acc = 0.f;
-    if (lane * 8 < D) {
+  const int items = Hq * P;
+  const RowPieces my(items);
+  if (my.sub >= my.tpb) return;
+  // A row's P lanes lie in one warp and run these loops together (items and
+  // step are multiples of P).
+  const unsigned lanes = P == 16 ? 0xffffu << (threadIdx.x & 16) : 0xffu << (threadIdx.x & 24);
+  for (long long t = t0 + static_cast<long long>(blockIdx.x - 1) * my.tpb + my.sub; t < t1;
+       t += static_cast<long long>(gridDim.x - 1) * my.tpb) {
+#pragma unroll 2
+    for (int i = my.first; i < items; i += my.step) {
+      const int h = i / P, c = i % P;
+      auto piece = [&](const Rows& x) {
+        return *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(x.p) + t * x.ts + h * x.hs + c * 8);
+      };
       const uint4 a4 = piece(o);
       const uint4 b4 = piece(dout);
       const uint4 r4 = resid.p ? piece(resid) : make_uint4(0, 0, 0, 0);
       const __nv_bfloat162* a2 = reinterpret_cast<const __nv_bfloat162*>(&a4);
       const __nv_bfloat162* b2 = reinterpret_cast<const __nv_bfloat162*>(&b4);
       const __nv_bfloat162* r2 = reinterpret_cast<const __nv_bfloat162*>(&r4);
+      float acc = 0.f;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const float2 fa = __bfloat1622float2(a2[k]);
@@ -873,38 +894,42 @@ __global__ void __launch_bounds__(256) packed_pre_kernel(const PlanArgs plan, Ro
         acc = fmaf(fa.x + fr.x, fb.x, acc);
         acc = fmaf(fa.y + fr.y, fb.y, acc);
       }
-    }
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
-    if (lane == 0) dsum[row] = acc;
-    float4* z = reinterpret_cast<float4*>(dq_acc + row * D);
-    for (int k = lane; k < D / 4; k += 32) z[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int off = P / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(lanes, acc, off);
+      const long long row = static_cast<long long>(h) * T + t;
+      if (c == 0) dsum[row] = acc;
+      float4* z = reinterpret_cast<float4*>(dq_acc + row * D + c * 8);
+      z[0] = make_float4(0.f, 0.f, 0.f, 0.f);
+      z[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
   }
 }
 
 // dq = bf16(scale * accumulator) for the packed rows, 8 elements per thread
 // and step; nothing when the plan found the offsets out of range.
-__global__ void __launch_bounds__(256) packed_post_kernel(const float* __restrict__ dq_acc, Rows dq, float scale,
-                                                          const PlanHeader* head, const int* __restrict__ cu, int S,
-                                                          int T, int Hq, int D) {
+template <int D>
+__global__ void __launch_bounds__(kRowThreads)
+    packed_post_kernel(const float* __restrict__ dq_acc, Rows dq, float scale, const PlanHeader* head,
+                       const int* __restrict__ cu, int S, int T, int Hq) {
   if (head->items == 0) return;
+  constexpr int P = D / 8;
   const int t0 = max(0, cu[0]), t1 = min(T, cu[S]);
-  const int pieces = D / 8;
-  const long long n = static_cast<long long>(t1 - t0) * Hq * pieces;
-  const long long stride = static_cast<long long>(gridDim.x) * blockDim.x;
-  for (long long e = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; e < n; e += stride) {
-    const long long th = e / pieces;
-    const int c = static_cast<int>(e - th * pieces);
-    const long long t = t0 + th / Hq;
-    const int h = static_cast<int>(th % Hq);
-    const float4* src = reinterpret_cast<const float4*>(dq_acc + (static_cast<long long>(h) * T + t) * D + c * 8);
-    const float4 x = src[0], y = src[1];
-    uint4 out;
-    out.x = pack_bf16x2(x.x * scale, x.y * scale);
-    out.y = pack_bf16x2(x.z * scale, x.w * scale);
-    out.z = pack_bf16x2(y.x * scale, y.y * scale);
-    out.w = pack_bf16x2(y.z * scale, y.w * scale);
-    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(dq.p) + t * dq.ts + h * dq.hs + c * 8) = out;
+  const int items = Hq * P;
+  const RowPieces my(items);
+  if (my.sub >= my.tpb) return;
+  for (long long t = t0 + static_cast<long long>(blockIdx.x) * my.tpb + my.sub; t < t1;
+       t += static_cast<long long>(gridDim.x) * my.tpb) {
+    for (int i = my.first; i < items; i += my.step) {
+      const int h = i / P, c = i % P;
+      const float4* src = reinterpret_cast<const float4*>(dq_acc + (static_cast<long long>(h) * T + t) * D + c * 8);
+      const float4 x = src[0], y = src[1];
+      uint4 out;
+      out.x = pack_bf16x2(x.x * scale, x.y * scale);
+      out.y = pack_bf16x2(x.z * scale, x.w * scale);
+      out.z = pack_bf16x2(y.x * scale, y.y * scale);
+      out.w = pack_bf16x2(y.z * scale, y.w * scale);
+      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(dq.p) + t * dq.ts + h * dq.hs + c * 8) = out;
+    }
   }
 }
 
@@ -934,7 +959,8 @@ cudaError_t launch_packed_bwd_t(const SeqShape& s, const PackedBwdLayout& x, con
                                 void* workspace, const LaunchCtl& ctl, cudaStream_t stream) {
   using C = BwdCfg<D>;
   auto kern = bwd_main_kernel<D, MASK, true>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  static SmemOnce once;
+  cudaError_t e = once.set(reinterpret_cast<const void*>(kern), C::kSmemBytes);
   if (e != cudaSuccess) return e;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   float* dsum = reinterpret_cast<float*>(ws + x.off_d);
@@ -949,12 +975,14 @@ cudaError_t launch_packed_bwd_t(const SeqShape& s, const PackedBwdLayout& x, con
   p.causal = s.causal;
   p.backward = 1;
   p.heads = s.Hkv;
+  p.sorted = x.max_items * s.Hkv > 148;
   p.head = reinterpret_cast<PlanHeader*>(ws + x.plan.head);
   p.items = reinterpret_cast<PlanItem*>(ws + x.plan.items);
   p.err = ctl.err;
   const long long rows = static_cast<long long>(s.T) * s.Hq;
-  packed_pre_kernel<D><<<1 + grid_for(rows, 8, 148 * 64), 256, 0, stream>>>(p, o, resid, dout, dsum, dq_acc, s.cu, s.S,
-                                                                            s.T, s.Hq);
+  const int row_blocks = grid_for(rows * (D / 8), kRowThreads, 148 * 64);
+  packed_pre_kernel<D><<<1 + row_blocks, kRowThreads, 0, stream>>>(p, o, resid, dout, dsum, dq_acc, s.cu, s.S, s.T,
+                                                                   s.Hq);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   BwdArgs a{};
   a.lse = lse;
@@ -976,8 +1004,7 @@ cudaError_t launch_packed_bwd_t(const SeqShape& s, const PackedBwdLayout& x, con
   if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   kern<<<static_cast<unsigned>(grid), kThreads, C::kSmemBytes, stream>>>(tq, tk, tv, tdo, tdk, tdv, a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  packed_post_kernel<<<grid_for(rows * D / 8, 256, 148 * 32), 256, 0, stream>>>(dq_acc, dq, s.scale, p.head, s.cu, s.S,
-                                                                               s.T, s.Hq, D);
+  packed_post_kernel<D><<<row_blocks, kRowThreads, 0, stream>>>(dq_acc, dq, s.scale, p.head, s.cu, s.S, s.T, s.Hq);
   return cudaGetLastError();
 }
 

@@ -2,6 +2,7 @@
 // launchers (fa_fwd.cu, fa_bwd.cu). Not installed, not part of the ABI.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda.h>
@@ -168,6 +169,22 @@ inline int page_box(int page) {
   while (b < 128 && page % (2 * b) == 0) b *= 2;
   return b;
 }
+
+// Sets a kernel's dynamic shared memory limit the first time that it is
+// launched on a device (the call costs a microsecond of host time).
+struct SmemOnce {
+  std::atomic<uint64_t> done{0};  // one bit per device
+  cudaError_t set(const void* kern, int bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
+  }
+};
 
 // Launches a kernel that may start beside the one before it on the stream
 // (programmatic dependent launch) and waits for it with pdl_wait().

@@ -33,6 +33,7 @@
 #include <math_constants.h>
 
 #include "fa_internal.h"
+#include "fa_merge.cuh"
 #include "fa_plan.cuh"
 #include "sm100.cuh"
 
@@ -614,8 +615,7 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, PkCfg<D>::kMinBlocks)
 }
 
 // Merges the parts of the units that were cut along their keys, one warp per
-// row: O = sum_s e^(L_s - L) O_s, L = log sum_s e^(L_s). Grid (KV heads,
-// groups of four rows, units).
+// row. Grid (KV heads, groups of four rows, units).
 template <int D>
 __global__ void __launch_bounds__(128) packed_merge_kernel(const PkArgs a) {
   pdl_wait();
@@ -630,35 +630,12 @@ __global__ void __launch_bounds__(128) packed_merge_kernel(const PkArgs a) {
   const int n_tok = a.cu ? a.cu[sp.seq + 1] - tok_base : 1;
   const int tok = sp.tok0 + t * a.TT + rt / a.r;
   if (rt >= a.TT * a.r || tok >= n_tok) return;
-  auto prow_of = [&](int p) { return (static_cast<long long>(sp.slot0 + p) * a.Hkv + kvh) * rows + rw; };
-  float mx = -CUDART_INF_F;
-  for (int p = lane; p < sp.parts; p += 32) mx = fmaxf(mx, a.part_l[prow_of(p)]);
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-  const float mz = mx == -CUDART_INF_F ? 0.f : mx;
-  float den = 0.f;
-  for (int p = lane; p < sp.parts; p += 32) den += expf(a.part_l[prow_of(p)] - mz);
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) den += __shfl_xor_sync(0xffffffffu, den, off);
-  const float L = mz + logf(den);
-  const float Lz = den == 0.f ? 0.f : L;
-  constexpr int VW = D / 32;
-  float acc[VW];
-#pragma unroll
-  for (int i = 0; i < VW; ++i) acc[i] = 0.f;
-  for (int p = 0; p < sp.parts; ++p) {
-    const long long pr = prow_of(p);
-    const float wt = expf(a.part_l[pr] - Lz);
-    if (wt == 0.f) continue;
-#pragma unroll
-    for (int i = 0; i < VW; ++i) acc[i] = fmaf(wt, a.part_o[pr * D + lane * VW + i], acc[i]);
-  }
   const int head = kvh * a.r + rt % a.r;
   const long long row = static_cast<long long>(tok_base) + tok;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.o.p) + row * a.o.ts + head * a.o.hs + lane * VW);
-#pragma unroll
-  for (int i = 0; i < VW / 2; ++i) dst[i] = pack_bf16x2(acc[2 * i], acc[2 * i + 1]);
-  if (lane == 0) a.lse[static_cast<long long>(head) * a.total + row] = L;
+  merge_row<D>(a.part_o, a.part_l, (static_cast<long long>(sp.slot0) * a.Hkv + kvh) * rows + rw,
+               static_cast<long long>(a.Hkv) * rows, sp.parts,
+               static_cast<__nv_bfloat16*>(a.o.p) + row * a.o.ts + head * a.o.hs,
+               a.lse + static_cast<long long>(head) * a.total + row, lane);
 }
 
 struct Layout {
@@ -702,7 +679,8 @@ cudaError_t launch_t(const SeqShape& s, const CacheShape* c, const Layout& x, co
                      cudaStream_t stream) {
   using C = PkCfg<D>;
   auto kern = packed_fwd_kernel<D, PAGED>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  static SmemOnce once;
+  cudaError_t e = once.set(reinterpret_cast<const void*>(kern), C::kSmemBytes);
   if (e != cudaSuccess) return e;
   if constexpr (C::T == 1) {
     // The register split hands out exactly what a launch at 128 registers
@@ -725,6 +703,7 @@ cudaError_t launch_t(const SeqShape& s, const CacheShape* c, const Layout& x, co
   p.causal = s.causal;
   p.heads = s.Hkv;
   p.split_ctas = x.max_parts > 0 ? sms : 0;
+  p.sorted = x.max_items * s.Hkv > static_cast<long long>(C::kMinBlocks) * sms;
   p.head = reinterpret_cast<PlanHeader*>(ws + x.plan.head);
   p.items = reinterpret_cast<PlanItem*>(ws + x.plan.items);
   p.slots = reinterpret_cast<int*>(ws + x.plan.slots);

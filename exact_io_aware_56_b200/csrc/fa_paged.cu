@@ -43,6 +43,7 @@
 #include <math_constants.h>
 
 #include "fa_internal.h"
+#include "fa_merge.cuh"
 #include "sm100.cuh"
 
 namespace fa {
@@ -612,25 +613,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Loads 2 or 4 consecutive floats (8- or 16-byte aligned) into registers.
-__device__ __forceinline__ void load_vec(const float* p, float (&x)[4]) {
-  const float4 t = *reinterpret_cast<const float4*>(p);
-  x[0] = t.x;
-  x[1] = t.y;
-  x[2] = t.z;
-  x[3] = t.w;
-}
-__device__ __forceinline__ void load_vec(const float* p, float (&x)[2]) {
-  const float2 t = *reinterpret_cast<const float2*>(p);
-  x[0] = t.x;
-  x[1] = t.y;
-}
-
 // Merges the partials of a unit's rows (every copy of every segment), one
-// warp per row; grid (S * Hkv, groups of four rows). 32 partials a step: each
-// lane takes one logsumexp, whose max and sum go through the warp; the
-// weighted sum of the partial O rows runs over d across lanes, eight partials
-// at a time so that their loads overlap.
+// warp per row; grid (S * Hkv, groups of four rows).
 template <int D>
 __global__ void __launch_bounds__(128)
     paged_few_merge_kernel(const Args a, int ctas, int rho, Rows o, float* __restrict__ lse) {
@@ -651,54 +635,11 @@ __global__ void __launch_bounds__(128)
   const int c0 = run_of(first, W, G);
   const int n_parts = (run_of(first + Tb - 1, W, G) - c0 + 1) * rho;
   // Partial p = (run c0 + p / rho, copy p % rho).
-  const long long base = (static_cast<long long>(blockIdx.x) + c0) * rho;
-  auto prow_of = [&](int p) -> long long { return (base + p) * a.rv + rr; };
-  constexpr int VW = D / 32;
-  float acc[VW], m = -CUDART_INF_F, den = 0.f;
-#pragma unroll
-  for (int i = 0; i < VW; ++i) acc[i] = 0.f;
-  for (int p0 = 0; p0 < n_parts; p0 += 32) {
-    const int cnt = min(32, n_parts - p0);
-    const float pl = lane < cnt ? a.part_l[prow_of(p0 + lane)] : -CUDART_INF_F;
-    float top = pl;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-    top = fmaxf(top, m);
-    const float ref = top == -CUDART_INF_F ? 0.f : top;  // no key so far: every weight 0
-    const float old = expf(m - ref);
-    const float wl = expf(pl - ref);
-    float sum = wl;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    den = den * old + sum;
-    m = top;
-#pragma unroll
-    for (int k = 0; k < VW; ++k) acc[k] *= old;
-    for (int i = 0; i < cnt; i += 8) {
-      float x[8][VW];
-#pragma unroll
-      for (int q = 0; q < 8; ++q)
-        if (i + q < cnt) load_vec(a.part_o + prow_of(p0 + i + q) * D + lane * VW, x[q]);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const float wq = __shfl_sync(0xffffffffu, wl, (i + q) & 31);
-        if (i + q < cnt && wq != 0.f)
-#pragma unroll
-          for (int k = 0; k < VW; ++k) acc[k] = fmaf(wq, x[q][k], acc[k]);
-      }
-    }
-  }
-  const float inv = den == 0.f ? 0.f : 1.f / den;
+  const long long row0 = (static_cast<long long>(blockIdx.x) + c0) * rho * a.rv + rr;
   const int tok = tok0 + rr / a.r;
   const int h = kvh * a.r + rr % a.r;
-  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(o.p) + tok * o.ts + h * o.hs + lane * VW;
-  if constexpr (VW == 4) {
-    *reinterpret_cast<uint2*>(dst) =
-        make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
-  } else {
-    *reinterpret_cast<uint32_t*>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-  }
-  if (lane == 0) lse[static_cast<long long>(h) * a.T + tok] = den == 0.f ? -CUDART_INF_F : m + logf(den);
+  merge_row<D>(a.part_o, a.part_l, row0, a.rv, n_parts, static_cast<__nv_bfloat16*>(o.p) + tok * o.ts + h * o.hs,
+               lse + static_cast<long long>(h) * a.T + tok, lane);
 }
 
 struct Plan {
@@ -730,7 +671,8 @@ cudaError_t launch_t(const SeqShape& s, const CacheShape& c, const Plan& p, cons
                      const LaunchCtl& ctl, cudaStream_t stream) {
   using C = Cfg<D>;
   auto kern = paged_few_kernel<D, RHO>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  static SmemOnce once;
+  cudaError_t e = once.set(reinterpret_cast<const void*>(kern), C::kSmemBytes);
   if (e != cudaSuccess) return e;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   Args a;

@@ -36,6 +36,7 @@ struct PlanArgs {
   int backward;    // items are key tiles of the backward, else query tokens of the forward
   int heads;       // CTAs per item (KV heads)
   int split_ctas;  // > 0: items may be cut so that this many CTAs are busy
+  int sorted;      // 0: every CTA is resident at once, any order does
   PlanHeader* head;
   PlanItem* items;
   int* slots;      // per item: its part's slot, -1 when the unit is whole (nullptr: not wanted)
@@ -72,7 +73,7 @@ __device__ __forceinline__ int plan_scan(int x, int* warp_sum, int& total) {
   __syncthreads();
   int before = 0;
   total = 0;
-#pragma unroll
+#pragma unroll 4
   for (int i = 0; i < NT / 32; ++i) {
     const int y = warp_sum[i];
     if (i < warp) before += y;
@@ -93,7 +94,9 @@ __host__ __device__ inline int plan_fwd_tiles(int n, int len, int tok0, int unit
   return last < 0 ? 1 : static_cast<int>(last / 128) + 1;
 }
 
-// Writes the list; one block of NT threads.
+// Writes the list; one block of NT threads. (Run once per call on cold
+// instruction caches, it costs by the length of its code: loops are kept
+// rolled, and the passes share theirs.)
 template <int NT>
 __device__ void plan_block(const PlanArgs& a, PlanShared& sh) {
   const int lane = threadIdx.x & 31;
@@ -138,17 +141,20 @@ __device__ void plan_block(const PlanArgs& a, PlanShared& sh) {
     if (a.backward) return (sh.n[lo] + 63) / 64 - (a.causal ? tok0 / 64 : 0);
     return plan_fwd_tiles(sh.n[lo], sh.len[lo], tok0, a.unit, a.causal);
   };
-  // f(seq, tok0, work) for every unit.
+  // f(u, seq, tok0, work) for every unit.
   int held_units = 0;
   auto each = [&](auto f) {
+    int base = 0;
 #pragma unroll 1
     for (int b0 = 0; b0 < a.S; b0 += kPlanSeqs) {
       const int units = one_chunk ? held_units : load(b0);
+#pragma unroll 1
       for (int u = threadIdx.x; u < units; u += NT) {
         int seq, tok0;
         const int w = unit_of(b0, u, seq, tok0);
-        f(seq, tok0, w);
+        f(base + u, seq, tok0, w);
       }
+      base += units;
       if (!one_chunk) __syncthreads();
     }
   };
@@ -174,6 +180,14 @@ __device__ void plan_block(const PlanArgs& a, PlanShared& sh) {
     }
     return;
   }
+  if (!a.sorted && a.split_ctas == 0) {
+    each([&](int u, int seq, int tok0, int w) {
+      a.items[u] = PlanItem{seq, tok0, 0, w};
+      if (a.slots) a.slots[u] = -1;
+    });
+    if (threadIdx.x == 0) *a.head = PlanHeader{U, 0, {0, 0}};
+    return;
+  }
   // Largest work there can be: sets the width of a bucket.
   long long most = a.backward ? a.T / 64 + 1 : a.max_len / 128 + 1;
   int L = 0x7fffffff;
@@ -184,7 +198,7 @@ __device__ void plan_block(const PlanArgs& a, PlanShared& sh) {
   if (a.split_ctas > 0 && static_cast<long long>(U) * a.heads < 2LL * a.split_ctas) {
     int my_max = 1;
     unsigned int my_sum = 0;  // below 2 * 148 units of at most 2^23 tiles: below 2^32
-    each([&](int, int, int w) {
+    each([&](int, int, int, int w) {
       my_max = max(my_max, w);
       my_sum += w;
     });
@@ -205,7 +219,7 @@ __device__ void plan_block(const PlanArgs& a, PlanShared& sh) {
       len[c] = c == 0 ? sh.most : static_cast<int>(fminf(fmaxf(l, 4.f), static_cast<float>(sh.most)));
       cnt[c] = 0;
     }
-    each([&](int, int, int w) {
+    each([&](int, int, int, int w) {
 #pragma unroll
       for (int c = 0; c < 8; ++c) cnt[c] += (w + len[c] - 1) / len[c];
     });
@@ -232,45 +246,43 @@ __device__ void plan_block(const PlanArgs& a, PlanShared& sh) {
   // Longest first: bucket 0 holds the longest.
   auto bucket = [&](int w) { return kPlanBuckets - 1 - (w >> shift); };
   auto parts_of = [&](int w) { return w <= L ? 1 : (w + L - 1) / L; };
-  each([&](int, int, int w) {
-    const int p = parts_of(w);
-    if (p == 1) {
-      atomicAdd(&sh.hist[bucket(w)], 1);
-    } else {
-      // p parts of nearly equal length: w % p of them one longer.
-      atomicAdd(&sh.hist[bucket(w / p)], p - w % p);
-      if (w % p) atomicAdd(&sh.hist[bucket(w / p + 1)], w % p);
-    }
-  });
-  __syncthreads();
+  // First pass: the buckets' sizes; second: the items, from their starts on.
   int run = 0;
 #pragma unroll 1
-  for (int i0 = 0; i0 < kPlanBuckets; i0 += NT) {
-    const int i = i0 + threadIdx.x;
-    const int h = sh.hist[i];
-    int total;
-    const int x = plan_scan<NT>(h, sh.warp_sum, total);
-    sh.hist[i] = run + x - h;
-    run += total;
+  for (int pass = 0; pass < 2; ++pass) {
+    each([&](int, int seq, int tok0, int w) {
+      const int p = parts_of(w);
+      int slot = -1;
+      if (pass == 1 && p > 1) {
+        slot = atomicAdd(&sh.n_slots, p);
+        a.split_list[atomicAdd(&sh.n_splits, 1)] = PlanSplit{seq, tok0, slot, p};
+      }
+      // p parts of nearly equal length: w % p of them one longer.
+      int j = 0;
+#pragma unroll 1
+      for (int k = 0; k < p; ++k) {
+        const int n = p == 1 ? w : w / p + (k < w % p ? 1 : 0);
+        const int at = atomicAdd(&sh.hist[bucket(n)], 1);
+        if (pass == 1) {
+          a.items[at] = PlanItem{seq, tok0, j, j + n};
+          if (a.slots) a.slots[at] = p > 1 ? slot + k : -1;
+        }
+        j += n;
+      }
+    });
+    __syncthreads();
+    if (pass == 1) break;
+#pragma unroll 1
+    for (int i0 = 0; i0 < kPlanBuckets; i0 += NT) {
+      const int i = i0 + threadIdx.x;
+      const int h = sh.hist[i];
+      int total;
+      const int x = plan_scan<NT>(h, sh.warp_sum, total);
+      sh.hist[i] = run + x - h;
+      run += total;
+    }
+    __syncthreads();
   }
-  __syncthreads();
-  each([&](int seq, int tok0, int w) {
-    const int p = parts_of(w);
-    int slot = -1;
-    if (p > 1) {
-      slot = atomicAdd(&sh.n_slots, p);
-      a.split_list[atomicAdd(&sh.n_splits, 1)] = PlanSplit{seq, tok0, slot, p};
-    }
-    int j = 0;
-    for (int k = 0; k < p; ++k) {
-      const int n = p == 1 ? w : w / p + (k < w % p ? 1 : 0);
-      const int at = atomicAdd(&sh.hist[bucket(n)], 1);
-      a.items[at] = PlanItem{seq, tok0, j, j + n};
-      if (a.slots) a.slots[at] = p > 1 ? slot + k : -1;
-      j += n;
-    }
-  });
-  __syncthreads();
   if (threadIdx.x == 0) *a.head = PlanHeader{run, sh.n_splits, {0, 0}};
 }
 
