@@ -120,7 +120,6 @@ struct BwdArgs {
   // Packed sequences only (N is then the rows T).
   const PlanHeader* head;
   const PlanItem* items;
-  const int* cu;
   Rows dk, dv;
   LaunchCtl ctl;
 };
@@ -195,12 +194,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   if constexpr (VAR) {
     static_assert(MASK != 2, "packed sequences: no mask or causal");
     const int item_no = blockIdx.x / a.Hkv;
+    const PlanItem item = load_item(a.items + item_no);
     if (item_no >= a.head->items) return;
-    const PlanItem item = a.items[item_no];
     bkv = blockIdx.x - item_no * a.Hkv;
     j = item.tok0 / kKT;
-    base = a.cu[item.seq];
-    N = a.cu[item.seq + 1] - base;
+    base = item.base;
+    N = item.n;
     nq = (N + kQT - 1) / kQT;
   } else if (MASK == 1 && a.band > 0) {
     // Bands of a.band key tiles, longest band first; within a band,
@@ -942,7 +941,7 @@ struct PackedBwdLayout {
 PackedBwdLayout packed_bwd_layout(const SeqShape& s) {
   PackedBwdLayout x;
   x.max_items = plan_max_units(s.S, s.T, kKT);
-  x.plan = plan_layout(x.max_items, 0);
+  x.plan = plan_layout(x.max_items, 0, 0);
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   x.off_d = up(x.plan.bytes);
   const size_t rows = static_cast<size_t>(s.T) * s.Hq;
@@ -996,7 +995,6 @@ cudaError_t launch_packed_bwd_t(const SeqShape& s, const PackedBwdLayout& x, con
   a.scale_log2 = s.scale * kLog2e;
   a.head = p.head;
   a.items = p.items;
-  a.cu = s.cu;
   a.dk = dk;
   a.dv = dv;
   a.ctl = ctl;

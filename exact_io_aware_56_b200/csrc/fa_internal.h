@@ -215,10 +215,16 @@ cudaError_t launch_paged_few(const SeqShape& s, const CacheShape& c, const Rows&
                              const Pages& v, float* lse, void* workspace, int sms, const LaunchCtl& ctl,
                              cudaStream_t stream);
 
-// Work list of the prompt kernels (forward: items of query tokens; backward:
-// key tiles), written by a one-block kernel into the workspace.
-struct PlanItem {
-  int seq, tok0, j0, j1;  // sequence, first token, key tiles [j0, j1) (backward: key tile j0)
+// Work item of the prompt kernels (fa_plan.cuh): all that a CTA needs to
+// start, in one load.
+struct alignas(16) PlanItem {
+  int base, n;   // the sequence's first row and its tokens
+  int off;       // place of its first token (paged), else 0
+  int tok0;      // first token of the item
+  int j0, j1;    // forward: key tiles; backward: [0, steps)
+  int slot;      // part of a unit cut along its keys, -1: whole unit
+  int seq;
+  int kvh;       // KV head, where the items carry it
 };
 
 size_t packed_fwd_workspace_bytes(const SeqShape& s, const CacheShape* c, int ctas);

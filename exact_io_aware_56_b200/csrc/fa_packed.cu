@@ -16,18 +16,27 @@
 //    head (rows in token-major order), so that grouped heads share each K/V
 //    tile in shared memory, short sequences fill their tiles r times better
 //    than one head per tile would, and the causal edge is cut at TT tokens.
-//  * The work comes from a list (fa_plan.cuh), longest first. A unit of few
-//    long rows (a chunk over a long cache, too few to fill the GPU) may be cut
-//    along its keys; its parts leave O / l and logsumexp in the workspace and
-//    a second kernel merges them.
+//  * The work comes from a list (fa_plan.cuh), longest first. CTAs stay
+//    resident and take items until none is left; the next item's first K/V
+//    tiles and Q load, and its first S products run, beside this one's last
+//    softmax and epilogue. (One CTA per item spent 5.9 us of 44 per item on
+//    starting, first loads and ending, at 16k packed tokens, d = 128.) Chunks
+//    over a cache that make too few units to fill the GPU evenly are instead
+//    cut into one run per CTA of equal cost; units that a run's end cuts along
+//    their keys leave O / l and logsumexp in the workspace and a second kernel
+//    merges them.
 //  * Tiles end where sequences do: scores of keys behind the end are replaced
 //    by -inf; the V rows there, which may hold anything (the next sequence,
 //    stale cache slots, NaN), are zeroed in shared memory before P V (warp
-//    kFixWarp); rows are stored whole tiles at a time by TMA, or row by row
-//    where the tile holds rows that are not this sequence's.
+//    kFixWarp). O leaves by TMA in whole tiles (at d = 128 that takes 0.8 us
+//    off an item against storing rows) or, where a tile holds rows that are
+//    not this sequence's, row by row.
 //
-// Warp roles (w0 = 4T): 0..w0-1 softmax, w0 Q and K producer, w0+1 MMA and
-// tensor memory, w0+2 V producer, w0+3 V rows behind the end.
+// Warp roles (w0 = 4T): 0..w0-1 softmax, w0 takes items and loads Q and K,
+// w0+1 MMA and tensor memory, w0+2 loads V, w0+3 zeroes V rows behind the end.
+// All rings and barrier phases run on across items. O_t needs no barrier of
+// its own between items: P V of the next item follows p_ready, which the
+// softmax warps of tile t give after their epilogue.
 
 #include <cuda_bf16.h>
 #include <math_constants.h>
@@ -42,10 +51,6 @@ namespace {
 
 constexpr int kBM = 128;  // rows per query tile
 constexpr int kBN = 128;  // keys per tile
-// Register split of the one-tile form (as fa_fwd.cu).
-constexpr int kSoftmaxRegs1 = 192;
-constexpr int kOtherRegs1 = 64;
-static_assert(kSoftmaxRegs1 + kOtherRegs1 == 2 * 128, "register split of the one-tile form");
 // Rescale thresholds of the running max, log2 units (as fa_fwd.cu: exact
 // where the residual is written, so that the backward's D is; else lazy).
 constexpr float kRescaleExact = 0.0f;
@@ -57,11 +62,18 @@ struct PkCfg {
   static constexpr bool SEP = D == 64;  // P in its own tensor-memory columns
   static constexpr int kThreads = T == 1 ? 256 : 384;
   static constexpr int kMinBlocks = T == 1 ? 2 : 1;
+  // Register shares (setmaxnreg) of a softmax warpgroup and of the other
+  // warps' group: together what the launch gives the CTA (128 per thread in
+  // two warpgroups, 168 in three).
+  static constexpr int kLaunchRegs = T == 1 ? 128 : 168;
+  static constexpr int kSoftmaxRegs = T == 1 ? 192 : 208;
+  static constexpr int kOtherRegs = T == 1 ? 64 : 88;
+  static_assert(T * kSoftmaxRegs + kOtherRegs == (T + 1) * kLaunchRegs, "register split");
   static constexpr int kProducerWarp = 4 * T;
   static constexpr int kMmaWarp = 4 * T + 1;
   static constexpr int kVProducerWarp = 4 * T + 2;
   static constexpr int kFixWarp = 4 * T + 3;
-  static constexpr int kKStages = T == 1 ? 2 : 3;
+  static constexpr int kKStages = 2;
   static constexpr int kVStages = 2;
   static constexpr int kBoxBytes = kBN * 128;
   static constexpr int kBoxes = D / 64;
@@ -69,12 +81,13 @@ struct PkCfg {
   static constexpr int kOffQ = 0;
   static constexpr int kOffK = T * kTileBytes;
   static constexpr int kOffV = kOffK + kKStages * kTileBytes;
-  static constexpr int kOffBar = kOffV + kVStages * kTileBytes;
+  // d = 128: whole output tiles leave by TMA through one 16-KB box (64
+  // columns) per tile; at d = 64 each thread stores its own row.
+  static constexpr bool kStaged = T == 2;
+  static constexpr int kOffStage = kOffV + kVStages * kTileBytes;
+  static constexpr int kOffBar = kOffStage + (kStaged ? T * 16384 : 0);
   static constexpr int kBarBytes = 512;
-  // Output staging: two 16-KB boxes per tile; the Q_t buffer at d = 128, the
-  // Q buffer and a box of its own at d = 64.
-  static constexpr int kOffStage = (kOffBar + kBarBytes + 1023) / 1024 * 1024;
-  static constexpr int kSmemBytes = (T == 1 ? kOffStage + 16384 : kOffBar + kBarBytes) + 1024;
+  static constexpr int kSmemBytes = kOffBar + kBarBytes + 1024;  // + alignment slack
   static constexpr uint32_t kTmemCols = T == 1 ? 256 : 512;
   static constexpr uint32_t kColO = T == 1 ? 128 : 256;
   static constexpr uint32_t kColP = 192;  // SEP
@@ -85,33 +98,36 @@ struct PkCfg {
 };
 
 struct PkArgs {
-  const PlanHeader* head;
+  PlanHeader* head;
   const PlanItem* items;
-  const int* slots;
+  const int* run_first;
   const PlanSplit* split_list;
-  const int* cu;
-  const int* lens;  // paged
-  const int* table;
+  const int* table;  // paged
   long long table_stride;
   int n_pages, page, pb;
   Rows o, resid;
   float* lse;
-  float* part_o;  // [slot][KV head][T * 128][D]
+  float* part_o;  // [slot][T * 128][D]
   float* part_l;
   int total, Hkv, r, TT, causal;
+  int sectors;  // o (and its residual) can be stored 32 bytes at a time
   float scale_log2, rescale_tau;
   LaunchCtl ctl;
 };
 
 struct PkBars {
-  uint64_t q_full;
-  uint64_t k_full[3], v_full[2], v_land[2], k_empty[3], v_empty[2];
+  uint64_t q_full[2], q_empty[2];
+  uint64_t k_full[2], k_empty[2];
+  uint64_t v_full[2], v_land[2], v_empty[2];
   uint64_t s_full[2], p_ready[2][2], o_final[2];
   uint64_t s_free, pv_done;
-  uint64_t epi_full[2][2], epi_free[2];  // epi_full: [tile][staging box]
+  uint64_t epi_full[2], epi_free[2];  // output staging
+  uint64_t item_full[2], item_empty[2];
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
+  alignas(16) int4 item[2][2];  // taken items, and their KV heads
+  int kvh[2];
 };
 static_assert(sizeof(PkBars) <= 512, "barrier block exceeds its shared-memory reservation");
 
@@ -120,6 +136,33 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PlanArg
   __shared__ PlanShared sh;
   pdl_launch_dependents();
   plan_block<kPlanThreads>(a, sh);
+}
+
+// An item as a CTA works on it: tile t holds tokens [tok_t[t], ...) and takes
+// the first n_t[t] of the item's n key tiles.
+struct Unit {
+  PlanItem it;
+  int kvh, n, n_t[2], tok_t[2];
+  __device__ __forceinline__ int len() const { return it.off + it.n; }
+  // Keys of the sequence in the item's u-th key tile (<= 0: none).
+  __device__ __forceinline__ int keys(int u) const { return min(kBN, len() - (it.j0 + u) * kBN); }
+};
+
+template <int T>
+__device__ __forceinline__ Unit make_unit(const PlanItem& it, int kvh, int TT, int causal) {
+  Unit x;
+  x.it = it;
+  x.kvh = kvh;
+  x.n_t[1] = 0;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    x.tok_t[t] = it.tok0 + t * TT;
+    x.n_t[t] = 0;
+    if (t < T && x.tok_t[t] < it.n)
+      x.n_t[t] = max(0, min(it.j1, plan_fwd_tiles(it.n, x.len(), x.tok_t[t], TT, causal)) - it.j0);
+  }
+  x.n = max(x.n_t[0], x.n_t[1]);
+  return x;
 }
 
 template <int D, bool PAGED>
@@ -141,24 +184,24 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, PkCfg<D>::kMinBlocks)
   const int lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    mbar_init(&bars->q_full, 1);
-    for (int s = 0; s < KS; ++s) {
-      mbar_init(&bars->k_full[s], 1);
-      mbar_init(&bars->k_empty[s], 1);
-    }
-    for (int s = 0; s < VS; ++s) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bars->q_full[s], 1);
+      mbar_init(&bars->q_empty[s], 1);
       mbar_init(&bars->v_full[s], 1);
       mbar_init(&bars->v_land[s], 1);
       mbar_init(&bars->v_empty[s], 1);
+      mbar_init(&bars->s_full[s], 1);
+      mbar_init(&bars->p_ready[s][0], kBM);
+      mbar_init(&bars->p_ready[s][1], kBM);
+      mbar_init(&bars->o_final[s], 1);
+      mbar_init(&bars->epi_full[s], kBM);
+      mbar_init(&bars->epi_free[s], 1);
+      mbar_init(&bars->item_full[s], 1);
+      mbar_init(&bars->item_empty[s], 4 * T + 3);  // softmax warps, MMA, V, fixer
     }
-    for (int t = 0; t < 2; ++t) {
-      mbar_init(&bars->s_full[t], 1);
-      mbar_init(&bars->p_ready[t][0], kBM);
-      mbar_init(&bars->p_ready[t][1], kBM);
-      mbar_init(&bars->o_final[t], 1);
-      mbar_init(&bars->epi_full[t][0], kBM);
-      mbar_init(&bars->epi_full[t][1], kBM);
-      mbar_init(&bars->epi_free[t], 1);
+    for (int s = 0; s < KS; ++s) {
+      mbar_init(&bars->k_full[s], 1);
+      mbar_init(&bars->k_empty[s], 1);
     }
     mbar_init(&bars->s_free, kBM);
     mbar_init(&bars->pv_done, 1);
@@ -176,42 +219,31 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, PkCfg<D>::kMinBlocks)
   // Everything above ran beside the plan.
   pdl_launch_dependents();
   pdl_wait();
-  const int item_no = blockIdx.x / a.Hkv;
-  if (item_no >= a.head->items) {
-    if (warp == C::kMmaWarp) tmem_dealloc(bars->tmem_base, C::kTmemCols);
-    return;
-  }
-  const int kvh = blockIdx.x - item_no * a.Hkv;
-  const PlanItem item = a.items[item_no];
-  const int tok_base = a.cu ? a.cu[item.seq] : item.seq;  // the sequence's first row
-  const int n_tok = a.cu ? a.cu[item.seq + 1] - tok_base : 1;
-  const int len = PAGED ? a.lens[item.seq] : n_tok;
-  const int off = len - n_tok;  // place of the first new token
-  // Tile t: tokens [tok0 + t TT, ...), key tiles [j0, j0 + n_t).
-  int n_t[2] = {0, 0}, tok_t[2];
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    tok_t[t] = item.tok0 + t * a.TT;
-    if (t < T && tok_t[t] < n_tok)
-      n_t[t] = max(0, min(item.j1, plan_fwd_tiles(n_tok, len, tok_t[t], a.TT, a.causal)) - item.j0);
-  }
-  const int n = max(n_t[0], n_t[1]);  // stream length
-
   const uint32_t tmem = bars->tmem_base;
   const Watch w{&bars->abort, a.ctl.err, a.ctl.budget_ns};
   auto all = [](bool b) { return __all_sync(0xffffffffu, b); };
 
-  // Copies key tile j of the sequence (K or V) to a stage; whole warp.
-  // Packed: one box per 64 columns. Paged: lane i copies part i.
-  auto keys_of = [&](int j) { return max(0, min(kBN, len - j * kBN)); };
-  auto page_of = [&](int j, int& slot) -> int {
+  // The i-th item of this CTA, from the producer; false: none is left, or a
+  // wait gave up. Whole warp.
+  auto next_unit = [&](int i, Unit& x) -> bool {
+    const int s = i & 1;
+    if (!all(wait_bar(&bars->item_full[s], (i >> 1) & 1, w))) return false;
+    const int4 p = bars->item[s][0], q = bars->item[s][1];
+    const int kvh = bars->kvh[s];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars->item_empty[s]);
+    x = make_unit<T>(PlanItem{p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w, kvh}, kvh, a.TT, a.causal);
+    return p.y > 0;
+  };
+  // Page and slot of this lane's part of the u-th key tile (paged).
+  auto page_of = [&](const Unit& x, int u, int& slot) -> int {
     slot = 0;
     int page_no = 0;
-    if (lane * a.pb < keys_of(j)) {
-      const int key = j * kBN + lane * a.pb;
+    if (lane * a.pb < x.keys(u)) {
+      const int key = (x.it.j0 + u) * kBN + lane * a.pb;
       const int pi = key / a.page;
       slot = key - pi * a.page;
-      page_no = a.table[static_cast<long long>(item.seq) * a.table_stride + pi];
+      page_no = a.table[static_cast<long long>(x.it.seq) * a.table_stride + pi];
       if (page_no < 0 || page_no >= a.n_pages) {
         page_no = a.n_pages;  // past the tensor: the copy fills zeros
         atomicOr(a.ctl.err, kErrData);
@@ -219,90 +251,138 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, PkCfg<D>::kMinBlocks)
     }
     return page_no;
   };
-  auto load_tile = [&](const CUtensorMap* tm, uint64_t* bar, uint8_t* dst, int j, int page_no, int slot) {
+  // Copies the u-th key tile (K or V) to a stage; whole warp. Packed: one box
+  // per 64 columns. Paged: lane i copies part i.
+  auto load_tile = [&](const CUtensorMap* tm, uint64_t* bar, uint8_t* dst, const Unit& x, int u, int page_no, int slot) {
     if constexpr (PAGED) {
-      const int parts = (keys_of(j) + a.pb - 1) / a.pb;
+      const int parts = (max(0, x.keys(u)) + a.pb - 1) / a.pb;
       if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(parts) * a.pb * 128u * C::kBoxes);
       __syncwarp();
       if (lane < parts)
 #pragma unroll
-        for (int x = 0; x < C::kBoxes; ++x)
-          tma_load_4d(tm, bar, dst + lane * a.pb * 128 + x * C::kBoxBytes, x * 64, slot, kvh, page_no);
+        for (int b = 0; b < C::kBoxes; ++b)
+          tma_load_4d(tm, bar, dst + lane * a.pb * 128 + b * C::kBoxBytes, b * 64, slot, x.kvh, page_no);
     } else if (lane == 0) {
       mbar_arrive_expect_tx(bar, C::kTileBytes);
 #pragma unroll
-      for (int x = 0; x < C::kBoxes; ++x)
-        tma_load_3d(tm, bar, dst + x * C::kBoxBytes, x * 64, tok_base + j * kBN, kvh);
+      for (int b = 0; b < C::kBoxes; ++b)
+        tma_load_3d(tm, bar, dst + b * C::kBoxBytes, b * 64, x.it.base + (x.it.j0 + u) * kBN, x.kvh);
     }
   };
 
   if (warp >= 4 * T) {
-    if constexpr (T == 1) regs_dec<kOtherRegs1>();
+    regs_dec<C::kOtherRegs>();
     if (warp == C::kProducerWarp) {
-      // ------------------------------------------------------- Q, K producer
-      int issued = 0;
+      // ------------------------------------------------ items, Q and K
       if (lane == 0) {
         tma_prefetch_desc(&tmQ);
         tma_prefetch_desc(&tmK);
-        const int tiles = T == 2 && n_t[1] > 0 ? 2 : 1;
-        mbar_arrive_expect_tx(&bars->q_full, static_cast<uint32_t>(tiles * C::kBoxes) * a.TT * a.r * 128u);
-        for (int t = 0; t < tiles; ++t)
-#pragma unroll
-          for (int x = 0; x < C::kBoxes; ++x)
-            tma_load_4d(&tmQ, &bars->q_full, smem + C::kOffQ + t * C::kTileBytes + x * C::kBoxBytes, x * 64, 0,
-                        tok_base + tok_t[t], kvh);
       }
-      __syncwarp();
-      for (int u = 0; u < n; ++u) {
-        const int s = u % KS;
-        int slot = 0, page_no = 0;
-        if constexpr (PAGED) page_no = page_of(item.j0 + u, slot);
-        if (u >= KS && !all(wait_bar(&bars->k_empty[s], (u / KS - 1) & 1, w))) break;
-        load_tile(&tmK, &bars->k_full[s], smem + C::kOffK + s * C::kTileBytes, item.j0 + u, page_no, slot);
-        issued = u + 1;
+      // Items of the list times the KV heads, taken one by one; or, where the
+      // plan cut the work into runs, this CTA's own items.
+      const bool runs = a.head->runs != 0;
+      int idx = runs ? a.run_first[blockIdx.x] : blockIdx.x;
+      const int total = runs ? a.run_first[blockIdx.x + 1] : a.head->items * a.Hkv;
+      int kg = 0, q_uses[2] = {0, 0};
+      bool ok = true;
+      for (int i = 0; ok; ++i) {
+        const int sl = i & 1;
+        const bool more = idx < total;
+        PlanItem it{};
+        if (more) it = load_item(a.items + (runs ? idx : idx / a.Hkv));
+        const int kvh = runs ? it.kvh : idx % a.Hkv;
+        if (i >= 2 && !all(wait_bar(&bars->item_empty[sl], ((i >> 1) - 1) & 1, w))) break;
+        int after = 0;
+        if (lane == 0) {
+          bars->item[sl][0] = make_int4(it.base, it.n, it.off, it.tok0);
+          bars->item[sl][1] = make_int4(it.j0, it.j1, it.slot, it.seq);
+          bars->kvh[sl] = kvh;
+          mbar_arrive(&bars->item_full[sl]);
+          if (more && !runs) after = atomicAdd(&a.head->taken, 1);  // arrives while this item's tiles load
+        }
+        if (!more) break;
+        const Unit x = make_unit<T>(it, kvh, a.TT, a.causal);
+        for (int u = 0; u < x.n; ++u) {
+          const int s = kg % KS;
+          int slot = 0, page_no = 0;
+          if constexpr (PAGED) page_no = page_of(x, u, slot);
+          if (kg >= KS && !(ok = all(wait_bar(&bars->k_empty[s], (kg / KS - 1) & 1, w)))) break;
+          load_tile(&tmK, &bars->k_full[s], smem + C::kOffK + s * C::kTileBytes, x, u, page_no, slot);
+          ++kg;
+          if (u > 0) continue;
+          // Q after the first key tile: its buffers free up later.
+#pragma unroll
+          for (int t = 0; t < T; ++t) {
+            if (x.n_t[t] == 0) continue;
+            if (q_uses[t] > 0 && !(ok = all(wait_bar(&bars->q_empty[t], (q_uses[t] - 1) & 1, w)))) break;
+            if (lane == 0) {
+              mbar_arrive_expect_tx(&bars->q_full[t], static_cast<uint32_t>(C::kBoxes) * a.TT * a.r * 128u);
+#pragma unroll
+              for (int b = 0; b < C::kBoxes; ++b)
+                tma_load_4d(&tmQ, &bars->q_full[t], smem + C::kOffQ + t * C::kTileBytes + b * C::kBoxBytes, b * 64, 0,
+                            it.base + x.tok_t[t], kvh);
+            }
+            ++q_uses[t];
+          }
+          if (!ok) break;
+        }
+        idx = runs ? idx + 1 : gridDim.x + __shfl_sync(0xffffffffu, after, 0);
       }
       // Every copy issued must land before the CTA may exit.
-      drain_bar(&bars->q_full, 0, w);
+#pragma unroll
+      for (int t = 0; t < T; ++t)
+        if (q_uses[t] > 0) drain_bar(&bars->q_full[t], (q_uses[t] - 1) & 1, w);
       for (int s = 0; s < KS; ++s)
-        if (issued > s) drain_bar(&bars->k_full[s], ((issued - 1 - s) / KS) & 1, w);
+        if (kg > s) drain_bar(&bars->k_full[s], ((kg - 1 - s) / KS) & 1, w);
     } else if (warp == C::kVProducerWarp) {
       // ----------------------------------------------------------- V producer
       if (lane == 0) tma_prefetch_desc(&tmV);
-      int issued = 0;
-      bool tail_issued = false;
-      for (int u = 0; u < n; ++u) {
-        const int s = u % VS;
-        int slot = 0, page_no = 0;
-        if constexpr (PAGED) page_no = page_of(item.j0 + u, slot);
-        if (u >= VS && !all(wait_bar(&bars->v_empty[s], (u / VS - 1) & 1, w))) break;
-        // Only the sequence's last key tile can be short.
-        const bool tail = keys_of(item.j0 + u) < kBN;
-        load_tile(&tmV, tail ? &bars->v_land[s] : &bars->v_full[s], smem + C::kOffV + s * C::kTileBytes, item.j0 + u,
-                  page_no, slot);
-        if (tail)
-          tail_issued = true;
-        else
-          issued = u + 1;
+      int vg = 0;
+      uint32_t tail_last = 0, land_par = 0;  // per stage: last use was a tail; parity of its next landing phase
+      bool ok = true;
+      Unit x;
+      for (int i = 0; ok && next_unit(i, x); ++i) {
+        for (int u = 0; u < x.n; ++u) {
+          const int s = vg % VS;
+          int slot = 0, page_no = 0;
+          if constexpr (PAGED) page_no = page_of(x, u, slot);
+          if (vg >= VS && !(ok = all(wait_bar(&bars->v_empty[s], (vg / VS - 1) & 1, w)))) break;
+          // Only a sequence's last key tile can be short.
+          const bool tail = x.keys(u) < kBN;
+          load_tile(&tmV, tail ? &bars->v_land[s] : &bars->v_full[s], smem + C::kOffV + s * C::kTileBytes, x, u, page_no,
+                    slot);
+          tail_last = tail ? tail_last | (1u << s) : tail_last & ~(1u << s);
+          if (tail) land_par ^= 1u << s;
+          ++vg;
+        }
       }
-      for (int s = 0; s < VS; ++s) {
-        if (issued > s) drain_bar(&bars->v_full[s], ((issued - 1 - s) / VS) & 1, w);
-        if (tail_issued && s == (n - 1) % VS) drain_bar(&bars->v_land[s], 0, w);
-      }
+      for (int s = 0; s < VS; ++s)
+        if (vg > s) {
+          if ((tail_last >> s) & 1)
+            drain_bar(&bars->v_land[s], ((land_par >> s) & 1) ^ 1, w);
+          else
+            drain_bar(&bars->v_full[s], ((vg - 1 - s) / VS) & 1, w);
+        }
     } else if (warp == C::kFixWarp) {
       // -------------------------- V rows behind the sequence's last key
-      const int keys = n > 0 ? keys_of(item.j0 + n - 1) : kBN;
-      if (keys < kBN) {
-        const int s = (n - 1) % VS;
-        if (all(wait_bar(&bars->v_land[s], 0, w))) {
+      int vg = 0;
+      uint32_t land_par = 0;
+      Unit x;
+      for (int i = 0; next_unit(i, x); ++i) {
+        vg += x.n;
+        const int keys = max(0, x.keys(x.n - 1));
+        if (keys == kBN) continue;
+        const int s = (vg - 1) % VS;
+        if (!all(wait_bar(&bars->v_land[s], (land_par >> s) & 1, w))) break;
+        land_par ^= 1u << s;
 #pragma unroll
-          for (int x = 0; x < C::kBoxes; ++x) {
-            uint4* box = reinterpret_cast<uint4*>(smem + C::kOffV + s * C::kTileBytes + x * C::kBoxBytes);
-            for (int i = keys * 8 + lane; i < kBN * 8; i += 32) box[i] = make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars->v_full[s]);
+        for (int b = 0; b < C::kBoxes; ++b) {
+          uint4* box = reinterpret_cast<uint4*>(smem + C::kOffV + s * C::kTileBytes + b * C::kBoxBytes);
+          for (int e = keys * 8 + lane; e < kBN * 8; e += 32) box[e] = make_uint4(0, 0, 0, 0);
         }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->v_full[s]);
       }
     } else if (warp == C::kMmaWarp) {
       // ----------------------------------------------------------- MMA issue
@@ -316,293 +396,326 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, PkCfg<D>::kMinBlocks)
       const uint64_t dK = sdesc_sw128(smem_u32(smem + C::kOffK), 16, 1024);
       const uint64_t dV = sdesc_sw128(smem_u32(smem + C::kOffV), C::kBoxBytes, 1024);
       auto ofs_kmaj = [](int k) { return static_cast<uint32_t>((k / 4) * C::kBoxBytes + (k % 4) * 32); };
-      auto issue_s = [&](int t, int u) {
+      // S_t = Q_t K^T, K in ring position g; `last`: the item's last use of Q_t.
+      auto issue_s = [&](int t, int g, bool last) {
         const uint64_t qa = sdesc_step(dQ, t * C::kTileBytes);
-        const uint64_t ka = sdesc_step(dK, (u % KS) * C::kTileBytes);
+        const uint64_t ka = sdesc_step(dK, (g % KS) * C::kTileBytes);
 #pragma unroll
         for (int k = 0; k < D / 16; k += 4)
           mma_ss_x4(tS[t], sdesc_step(qa, ofs_kmaj(k)), sdesc_step(qa, ofs_kmaj(k + 1)), sdesc_step(qa, ofs_kmaj(k + 2)),
                     sdesc_step(qa, ofs_kmaj(k + 3)), sdesc_step(ka, ofs_kmaj(k)), sdesc_step(ka, ofs_kmaj(k + 1)),
                     sdesc_step(ka, ofs_kmaj(k + 2)), sdesc_step(ka, ofs_kmaj(k + 3)), idesc_qk, k > 0, leader);
         mma_commit(&bars->s_full[t], leader);
+        if (last) mma_commit(&bars->q_empty[t], leader);
       };
-      // Half h of P V: keys [64h, 64h + 64).
-      auto issue_pv = [&](int t, int u, int h) {
-        const uint64_t va = sdesc_step(dV, (u % VS) * C::kTileBytes);
+      // Half h of O_t += P_t V (keys [64h, 64h + 64)), V in ring position g.
+      auto issue_pv = [&](int t, int g, int h, bool first) {
+        const uint64_t va = sdesc_step(dV, (g % VS) * C::kTileBytes);
         const int k = h * 4;
         mma_ts_x4(tO[t], tP[t] + k * 8, tP[t] + (k + 1) * 8, tP[t] + (k + 2) * 8, tP[t] + (k + 3) * 8,
                   sdesc_step(va, k * 2048), sdesc_step(va, (k + 1) * 2048), sdesc_step(va, (k + 2) * 2048),
-                  sdesc_step(va, (k + 3) * 2048), idesc_pv, (u > 0 || k > 0) ? 1u : 0u, leader);
+                  sdesc_step(va, (k + 3) * 2048), idesc_pv, (!first || k > 0) ? 1u : 0u, leader);
       };
-      bool ok = all(wait_bar(&bars->q_full, 0, w));
-      if (ok && n > 0) ok = all(wait_bar(&bars->k_full[0], 0, w));
-      if (ok && n > 0) {
-        tc_fence_after();
-#pragma unroll
-        for (int t = 0; t < T; ++t)
-          if (n_t[t] > 0) issue_s(t, 0);
-        mma_commit(&bars->k_empty[0], leader);
-      }
-      for (int u = 0; ok && u < n; ++u) {
-        const int s = u % VS;
-        const uint32_t par = (u / VS) & 1;
-        const int un = u + 1;
-        if constexpr (SEP) {
-          // S of the next key tile once the softmax has loaded this one.
-          if (un < n) {
-            if (!(ok = all(wait_bar(&bars->s_free, u & 1, w)) && all(wait_bar(&bars->k_full[un % KS], (un / KS) & 1, w))))
-              break;
-            tc_fence_after();
-            issue_s(0, un);
-            mma_commit(&bars->k_empty[un % KS], leader);
-          }
-        }
+      // Ring position (K and V alike), and per query tile its key tiles and
+      // items so far: the phases of the barriers.
+      int g0 = 0, c_t[2] = {0, 0}, i_t[2] = {0, 0};
+      bool ok = true;
+      Unit x;
+      for (int i = 0; ok && next_unit(i, x); ++i) {
+        if (!(ok = all(wait_bar(&bars->k_full[g0 % KS], (g0 / KS) & 1, w)))) break;
 #pragma unroll
         for (int t = 0; t < T; ++t) {
-          if (u >= n_t[t]) continue;
-          const bool last_user = t == T - 1 || u >= n_t[T - 1];
-          if (!(ok = all(wait_bar(&bars->p_ready[t][0], u & 1, w)) && all(wait_bar(&bars->v_full[s], par, w)))) break;
+          if (x.n_t[t] == 0) continue;
+          if (!(ok = all(wait_bar(&bars->q_full[t], i_t[t] & 1, w)))) break;
           tc_fence_after();
-          issue_pv(t, u, 0);
-          if (!(ok = all(wait_bar(&bars->p_ready[t][1], u & 1, w)))) break;
-          tc_fence_after();
-          issue_pv(t, u, 1);
-          if constexpr (SEP) mma_commit(&bars->pv_done, leader);
-          if (last_user) mma_commit(&bars->v_empty[s], leader);
-          if (u == n_t[t] - 1) mma_commit(&bars->o_final[t], leader);
-          if (!SEP && un < n_t[t]) {
-            if (!(ok = all(wait_bar(&bars->k_full[un % KS], (un / KS) & 1, w)))) break;
+          issue_s(t, g0, x.n_t[t] == 1);
+          ++i_t[t];
+        }
+        if (!ok) break;
+        mma_commit(&bars->k_empty[g0 % KS], leader);
+        for (int u = 0; ok && u < x.n; ++u) {
+          const int g = g0 + u;
+          const int s = g % VS;
+          const uint32_t par = (g / VS) & 1;
+          const int un = u + 1, gn = g + 1;
+          if constexpr (SEP) {
+            // S of the next key tile once the softmax has loaded this one.
+            if (un < x.n) {
+              if (!(ok = all(wait_bar(&bars->s_free, (c_t[0] + u) & 1, w)) && all(wait_bar(&bars->k_full[gn % KS], (gn / KS) & 1, w))))
+                break;
+              tc_fence_after();
+              issue_s(0, gn, un == x.n - 1);
+              mma_commit(&bars->k_empty[gn % KS], leader);
+            }
+          }
+#pragma unroll
+          for (int t = 0; t < T; ++t) {
+            if (u >= x.n_t[t]) continue;
+            const uint32_t pp = (c_t[t] + u) & 1;
+            if (!(ok = all(wait_bar(&bars->p_ready[t][0], pp, w)) && all(wait_bar(&bars->v_full[s], par, w)))) break;
             tc_fence_after();
-            issue_s(t, un);
-            if (t == T - 1 || un >= n_t[T - 1]) mma_commit(&bars->k_empty[un % KS], leader);
+            issue_pv(t, g, 0, u == 0);
+            if (!(ok = all(wait_bar(&bars->p_ready[t][1], pp, w)))) break;
+            tc_fence_after();
+            issue_pv(t, g, 1, u == 0);
+            if constexpr (SEP) mma_commit(&bars->pv_done, leader);
+            if (t == T - 1 || u >= x.n_t[T - 1]) mma_commit(&bars->v_empty[s], leader);
+            if (u == x.n_t[t] - 1) mma_commit(&bars->o_final[t], leader);
+            if (!SEP && un < x.n_t[t]) {
+              if (!(ok = all(wait_bar(&bars->k_full[gn % KS], (gn / KS) & 1, w)))) break;
+              tc_fence_after();
+              issue_s(t, gn, un == x.n_t[t] - 1);
+              if (t == T - 1 || un >= x.n_t[T - 1]) mma_commit(&bars->k_empty[gn % KS], leader);
+            }
           }
         }
+        g0 += x.n;
+#pragma unroll
+        for (int t = 0; t < T; ++t) c_t[t] += x.n_t[t];
       }
       // All MMAs issued by this thread must finish before tensor memory is freed.
       mma_commit(&bars->drain, leader);
       all(drain_bar(&bars->drain, 0, w));
     }
   } else {
-    if constexpr (T == 1) regs_inc<kSoftmaxRegs1>();
+    regs_inc<C::kSoftmaxRegs>();
     // ------------------------------------------------------------- softmax
     const int t = warp >> 2;
     const int quad = warp & 3;
     const int rw = quad * 32 + lane;  // row of the tile: token rw / r, head rw % r
+    const int rw_tok = rw / a.r;
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t tS = tmem + lane_off + t * 128u;
     const uint32_t tPw = SEP ? tmem + lane_off + C::kColP : tS;
     const uint32_t tO = tmem + lane_off + C::kColO + t * D;
-    const int nt = T == 2 && t == 1 ? n_t[1] : n_t[0];
-    const int tok0 = T == 2 && t == 1 ? tok_t[1] : tok_t[0];
-    const int tok = tok0 + rw / a.r;
-    const bool mine = rw < a.TT * a.r && tok < n_tok;
-    // Last visible key of this row, and of the tile's first.
-    const int lim = a.causal ? min(off + tok, len - 1) : len - 1;
-    const int lim0 = a.causal ? min(off + tok0, len - 1) : len - 1;
     const float sl2 = a.scale_log2;
-    float m = -CUDART_INF_F;
-    float l = 0.f;
+    uint8_t* const stage = smem + C::kOffStage + t * 16384;
+    const bool issuer = rw == 0;
+    int c = 0, items = 0, boxes = 0;  // key tiles, items and staged boxes so far: the phases of the barriers
     bool ok = true;
-    for (int u = 0; u < nt; ++u) {
-      ok = all(wait_bar(&bars->s_full[t], u & 1, w));
+    Unit x;
+    for (int i = 0; ok && next_unit(i, x); ++i) {
+      const int nt = T == 2 && t == 1 ? x.n_t[1] : x.n_t[0];
+      const int tok0 = T == 2 && t == 1 ? x.tok_t[1] : x.tok_t[0];
+      const int tok = tok0 + rw_tok;
+      // Last visible key of this row, and of the tile's first.
+      const int lim = a.causal ? min(x.it.off + tok, x.len() - 1) : x.len() - 1;
+      const int lim0 = a.causal ? min(x.it.off + tok0, x.len() - 1) : x.len() - 1;
+      float m = -CUDART_INF_F;
+      float l = 0.f;
+      for (int u = 0; u < nt; ++u) {
+        ok = all(wait_bar(&bars->s_full[t], (c + u) & 1, w));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t sr[kBN];
+        tmem_ld64x2(tS, sr);  // (no instruction may name more registers than the launch's share)
+        if constexpr (SEP) {
+          tc_fence_before();
+          mbar_arrive(&bars->s_free);
+        }
+        const int k0 = (x.it.j0 + u) * kBN;
+        if (k0 + kBN - 1 > lim0) {
+#pragma unroll
+          for (int e = 0; e < kBN; ++e)
+            if (k0 + e > lim) sr[e] = __float_as_uint(-CUDART_INF_F);
+        }
+        // Row max as 8 independent partial maxima of three-input max.
+        float pm[8];
+#pragma unroll
+        for (int y = 0; y < 8; ++y) pm[y] = fmaxf(__uint_as_float(sr[y]), __uint_as_float(sr[8 + y]));
+#pragma unroll
+        for (int e = 16; e < kBN; e += 16)
+#pragma unroll
+          for (int y = 0; y < 8; ++y)
+            pm[y] = fmax3(pm[y], __uint_as_float(sr[e + y]), __uint_as_float(sr[e + 8 + y]));
+        pm[0] = fmax3(pm[0], pm[1], pm[2]);
+        pm[3] = fmax3(pm[3], pm[4], pm[5]);
+        pm[6] = fmaxf(pm[6], pm[7]);
+        const float m_cand = fmax3(pm[0], pm[3], pm[6]) * sl2;
+        bool rescale = false;
+        float alpha = 1.f;
+        if (u == 0) {
+          m = m_cand;  // -inf for a row that sees no key of this tile
+        } else if (__any_sync(0xffffffffu, m_cand > m + a.rescale_tau)) {
+          const float m_new = fmaxf(m, m_cand);
+          alpha = m_new == -CUDART_INF_F ? 1.f : exp2_accurate(m - m_new);
+          m = m_new;
+          l *= alpha;
+          rescale = true;
+        }
+        const float neg_m = m == -CUDART_INF_F ? 0.f : -m;
+        if constexpr (SEP) {
+          // (Before an item's first tile the last item's o_final has said so.)
+          if (u > 0) {
+            ok = all(wait_bar(&bars->pv_done, (c + u - 1) & 1, w));
+            if (!ok) break;
+            tc_fence_after();
+          }
+        }
+        float ps[8];
+#pragma unroll
+        for (int y = 0; y < 8; ++y) ps[y] = 0.f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int b = 2 * h; b < 2 * h + 2; ++b) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float x0, x1;
+              ffma2(x0, x1, __uint_as_float(sr[b * 32 + 2 * e]), __uint_as_float(sr[b * 32 + 2 * e + 1]), sl2, sl2,
+                    neg_m, neg_m);
+              // Shares of the FMA pipe as in fa_fwd.cu (2 of 32 at d = 128,
+              // none at d = 64 causal).
+              constexpr int kPoly = D == 128 ? 2 : 0;
+              const float p0 = (2 * e < kPoly) ? exp2_poly(x0) : ex2(x0);
+              const float p1 = (2 * e + 1 < kPoly) ? exp2_poly(x1) : ex2(x1);
+              fadd2(ps[(2 * e) & 7], ps[(2 * e + 1) & 7], ps[(2 * e) & 7], ps[(2 * e + 1) & 7], p0, p1);
+              // bf16: the type of V, which the weights meet in P V.
+              pk[e] = pack_bf16x2(p0, p1);
+            }
+            tmem_st16(tPw + b * 16, pk);
+          }
+          if (h == 0 && rescale) {
+#pragma unroll
+            for (int b = 0; b < D / 32; ++b) {
+              uint32_t o32[32];
+              tmem_ld32(tO + b * 32, o32);
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                float y0, y1;
+                fmul2(y0, y1, __uint_as_float(o32[e]), __uint_as_float(o32[e + 1]), alpha, alpha);
+                o32[e] = __float_as_uint(y0);
+                o32[e + 1] = __float_as_uint(y1);
+              }
+              tmem_st32(tO + b * 32, o32);
+            }
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(&bars->p_ready[t][h]);
+        }
+        l += ((ps[0] + ps[1]) + (ps[2] + ps[3])) + ((ps[4] + ps[5]) + (ps[6] + ps[7]));
+      }
+      if (ok && nt > 0) {
+        ok = all(wait_bar(&bars->o_final[t], items & 1, w));
+        ++items;
+        c += nt;
+      }
       if (!ok) break;
       tc_fence_after();
-      uint32_t sr[kBN];
-      if constexpr (T == 1)
-        tmem_ld64x2(tS, sr);
-      else
-        tmem_ld128(tS, sr);
-      if constexpr (SEP) {
-        tc_fence_before();
-        mbar_arrive(&bars->s_free);
-      }
-      const int k0 = (item.j0 + u) * kBN;
-      if (k0 + kBN - 1 > lim0) {
-#pragma unroll
-        for (int i = 0; i < kBN; ++i)
-          if (k0 + i > lim) sr[i] = __float_as_uint(-CUDART_INF_F);
-      }
-      // Row max as 8 independent partial maxima of three-input max.
-      float pm[8];
-#pragma unroll
-      for (int x = 0; x < 8; ++x) pm[x] = fmaxf(__uint_as_float(sr[x]), __uint_as_float(sr[8 + x]));
-#pragma unroll
-      for (int i = 16; i < kBN; i += 16)
-#pragma unroll
-        for (int x = 0; x < 8; ++x)
-          pm[x] = fmax3(pm[x], __uint_as_float(sr[i + x]), __uint_as_float(sr[i + 8 + x]));
-      pm[0] = fmax3(pm[0], pm[1], pm[2]);
-      pm[3] = fmax3(pm[3], pm[4], pm[5]);
-      pm[6] = fmaxf(pm[6], pm[7]);
-      const float m_cand = fmax3(pm[0], pm[3], pm[6]) * sl2;
-      bool rescale = false;
-      float alpha = 1.f;
-      if (u == 0) {
-        m = m_cand;  // -inf for a row that sees no key of this tile
-      } else if (__any_sync(0xffffffffu, m_cand > m + a.rescale_tau)) {
-        const float m_new = fmaxf(m, m_cand);
-        alpha = m_new == -CUDART_INF_F ? 1.f : exp2_accurate(m - m_new);
-        m = m_new;
-        l *= alpha;
-        rescale = true;
-      }
-      const float neg_m = m == -CUDART_INF_F ? 0.f : -m;
-      if constexpr (SEP) {
-        if (u > 0) {
-          ok = all(wait_bar(&bars->pv_done, (u - 1) & 1, w));
-          if (!ok) break;
-          tc_fence_after();
-        }
-      }
-      float ps[8];
-#pragma unroll
-      for (int x = 0; x < 8; ++x) ps[x] = 0.f;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-#pragma unroll
-        for (int c = 2 * h; c < 2 * h + 2; ++c) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float x0, x1;
-            ffma2(x0, x1, __uint_as_float(sr[c * 32 + 2 * i]), __uint_as_float(sr[c * 32 + 2 * i + 1]), sl2, sl2,
-                  neg_m, neg_m);
-            // Shares of the FMA pipe as in fa_fwd.cu (2 of 32 at d = 128,
-            // none at d = 64 causal).
-            constexpr int kPoly = D == 128 ? 2 : 0;
-            const float p0 = (2 * i < kPoly) ? exp2_poly(x0) : ex2(x0);
-            const float p1 = (2 * i + 1 < kPoly) ? exp2_poly(x1) : ex2(x1);
-            fadd2(ps[(2 * i) & 7], ps[(2 * i + 1) & 7], ps[(2 * i) & 7], ps[(2 * i + 1) & 7], p0, p1);
-            // bf16: the type of V, which the weights meet in P V.
-            pk[i] = pack_bf16x2(p0, p1);
-          }
-          tmem_st16(tPw + c * 16, pk);
-        }
-        if (h == 0 && rescale) {
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t o32[32];
-            tmem_ld32(tO + c * 32, o32);
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              float y0, y1;
-              fmul2(y0, y1, __uint_as_float(o32[i]), __uint_as_float(o32[i + 1]), alpha, alpha);
-              o32[i] = __float_as_uint(y0);
-              o32[i + 1] = __float_as_uint(y1);
-            }
-            tmem_st32(tO + c * 32, o32);
-          }
-        }
-        tmem_st_wait();
-        tc_fence_before();
-        mbar_arrive(&bars->p_ready[t][h]);
-      }
-      l += ((ps[0] + ps[1]) + (ps[2] + ps[3])) + ((ps[4] + ps[5]) + (ps[6] + ps[7]));
-    }
-    if (ok && nt > 0) ok = all(wait_bar(&bars->o_final[t], 0, w));
-    if (ok) {
-      tc_fence_after();
+      const bool mine = rw < a.TT * a.r && tok < x.it.n;
       const float inv_l = l == 0.f ? 0.f : 1.f / l;  // 0: no visible key (O is 0 there, or never written)
       const float L = l == 0.f ? -CUDART_INF_F : (m + lg2(l)) * 0.69314718055994530942f;
-      const int slot = a.slots[item_no];
-      const long long row = static_cast<long long>(tok_base) + tok;
-      const int head = kvh * a.r + rw % a.r;
+      const long long row = static_cast<long long>(x.it.base) + tok;
+      const int head = x.kvh * a.r + rw - rw_tok * a.r;
       // 64 columns of this row's O, normalised.
-      auto load_o = [&](int x, uint32_t (&oo)[64]) {
+      auto load_o = [&](int b, uint32_t (&oo)[64]) {
         uint32_t(&o0)[32] = *reinterpret_cast<uint32_t(*)[32]>(&oo[0]);
         uint32_t(&o1)[32] = *reinterpret_cast<uint32_t(*)[32]>(&oo[32]);
         if (nt == 0) {
           // A part of the unit's keys that this tile's rows do not reach.
 #pragma unroll
-          for (int i = 0; i < 64; ++i) oo[i] = 0u;
+          for (int e = 0; e < 64; ++e) oo[e] = 0u;
           return;
         }
-        tmem_ld32_nowait(tO + x * 64, o0);
-        tmem_ld32_nowait(tO + x * 64 + 32, o1);
+        tmem_ld32_nowait(tO + b * 64, o0);
+        tmem_ld32_nowait(tO + b * 64 + 32, o1);
         tmem_ld_wait(o0);
         tmem_ld_tie(o1);
 #pragma unroll
-        for (int i = 0; i < 64; ++i) oo[i] = __float_as_uint(__uint_as_float(oo[i]) * inv_l);
+        for (int e = 0; e < 64; ++e) oo[e] = __float_as_uint(__uint_as_float(oo[e]) * inv_l);
       };
-      // Eight columns as bf16, or their rounding residual.
-      auto pack8 = [](const uint32_t* y, bool resid) {
-        uint4 v;
-        uint32_t* pv = reinterpret_cast<uint32_t*>(&v);
+      if (PAGED && x.it.slot >= 0) {
+        const long long prow = static_cast<long long>(x.it.slot) * (T * kBM) + t * kBM + rw;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float x0 = __uint_as_float(y[2 * e]), x1 = __uint_as_float(y[2 * e + 1]);
-          pv[e] = pack_bf16x2(x0, x1);
-          if (resid) {
-            const __nv_bfloat162 hi = *reinterpret_cast<const __nv_bfloat162*>(&pv[e]);
-            pv[e] = pack_bf16x2(x0 - __low2float(hi), x1 - __high2float(hi));
-          }
-        }
-        return v;
-      };
-      if (PAGED && slot >= 0) {
-        const long long prow = (static_cast<long long>(slot) * a.Hkv + kvh) * (T * kBM) + t * kBM + rw;
-#pragma unroll
-        for (int x = 0; x < D / 64; ++x) {
+        for (int b = 0; b < D / 64; ++b) {
           uint32_t oo[64];
-          load_o(x, oo);
-          if (mine) {
-            uint4* dst = reinterpret_cast<uint4*>(a.part_o + prow * D + x * 64);
+          load_o(b, oo);
+          if (mine)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) dst[i] = make_uint4(oo[4 * i], oo[4 * i + 1], oo[4 * i + 2], oo[4 * i + 3]);
-          }
+            for (int e = 0; e < 64; e += 8)
+              store_sector(a.part_o + prow * D + b * 64 + e, *reinterpret_cast<uint32_t(*)[8]>(&oo[e]));
+          __syncwarp();
         }
         if (mine) a.part_l[prow] = L;
-      } else {
-        constexpr int kBoxesO = D / 64;
-        const int jobs = kBoxesO * (a.resid.p ? 2 : 1);
-        if (tok0 + a.TT <= n_tok) {
-          // A whole tile: boxes staged in shared memory in the tensor map's
-          // swizzle and stored by TMA, two at a time (as fa_fwd.cu).
-          uint8_t* const slots[2] = {smem + C::kOffQ + (T == 1 ? 0 : t * C::kTileBytes),
-                                     T == 1 ? smem + C::kOffStage : smem + C::kOffQ + t * C::kTileBytes + 16384};
-          const bool issuer = rw == 0;
-          for (int i = 0; i < jobs; ++i) {
-            const int x = i % kBoxesO;
-            const bool resid = i >= kBoxesO;
-            uint8_t* st = slots[i % 2];
-            if (i >= 2 && !(ok = all(wait_bar(&bars->epi_free[t], (i - 2) & 1, w)))) break;
-            uint32_t oo[64];
-            load_o(x, oo);
+        continue;
+      }
+      // 16 columns as bf16 (or their rounding residual), two per register.
+      auto pack16 = [](const uint32_t* y, bool resid, uint32_t (&v)[8]) {
 #pragma unroll
-            for (int cc = 0; cc < 8; ++cc)
-              *reinterpret_cast<uint4*>(st + rw * 128 + ((cc ^ (rw & 7)) << 4)) = pack8(oo + 8 * cc, resid);
-            fence_proxy_async_smem();
-            // A barrier for each box: a fast warp arrives for the second
-            // before a slow one has for the first.
-            mbar_arrive(&bars->epi_full[t][i & 1]);
-            // (On a timeout every lane leaves at the next wait for epi_free.)
-            if (issuer && (ok = wait_bar(&bars->epi_full[t][i & 1], (i >> 1) & 1, w))) {
-              tma_store_4d(resid ? &tmR : &tmO, st, x * 64, 0, tok_base + tok0, kvh);
-              bulk_commit();
-              if (i + 1 < jobs && i + 1 >= 2) {
-                bulk_wait_read<1>();
-                mbar_arrive(&bars->epi_free[t]);
+        for (int e = 0; e < 8; ++e) {
+          const float x0 = __uint_as_float(y[2 * e]), x1 = __uint_as_float(y[2 * e + 1]);
+          v[e] = pack_bf16x2(x0, x1);
+          if (resid) {
+            const __nv_bfloat162 hi = *reinterpret_cast<const __nv_bfloat162*>(&v[e]);
+            v[e] = pack_bf16x2(x0 - __low2float(hi), x1 - __high2float(hi));
+          }
+        }
+      };
+      constexpr int kBoxesO = D / 64;
+      const int jobs = kBoxesO * (a.resid.p ? 2 : 1);
+      if (C::kStaged && tok0 + a.TT <= x.it.n) {
+        // A whole tile: boxes of 64 columns staged in the tensor map's swizzle.
+        for (int b = 0; b < jobs; ++b, ++boxes) {
+          const int col = b % kBoxesO;
+          const bool resid = b >= kBoxesO;
+          uint32_t oo[64];
+          load_o(col, oo);
+          if (boxes > 0) {
+            // The staged box before this one has been read.
+            if (issuer) {
+              bulk_wait_read<0>();
+              mbar_arrive(&bars->epi_free[t]);
+            }
+            __syncwarp();
+            if (!(ok = all(wait_bar(&bars->epi_free[t], (boxes - 1) & 1, w)))) break;
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t v[8];
+            pack16(oo + 16 * e, resid, v);
+            *reinterpret_cast<uint4*>(stage + rw * 128 + (((2 * e) ^ (rw & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<uint4*>(stage + rw * 128 + (((2 * e + 1) ^ (rw & 7)) << 4)) = make_uint4(v[4], v[5], v[6], v[7]);
+          }
+          fence_proxy_async_smem();
+          mbar_arrive(&bars->epi_full[t]);
+          // (After a timeout every lane leaves at a wait below or above.)
+          if (issuer && wait_bar(&bars->epi_full[t], boxes & 1, w)) {
+            tma_store_4d(resid ? &tmR : &tmO, stage, col * 64, 0, x.it.base + tok0, x.kvh);
+            bulk_commit();
+          }
+          __syncwarp();
+        }
+      } else if (tok0 < x.it.n) {
+        // Each thread stores its own row, whole 32-byte sectors at a time
+        // where the view's alignment allows it.
+        for (int b = 0; b < jobs; ++b) {
+          const int col = b % kBoxesO;
+          const bool resid = b >= kBoxesO;
+          uint32_t oo[64];
+          load_o(col, oo);
+          if (mine) {
+            const Rows& out = resid ? a.resid : a.o;
+            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(out.p) + row * out.ts + head * out.hs + col * 64;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t v[8];
+              pack16(oo + 16 * e, resid, v);
+              if (a.sectors) {
+                store_sector(dst + 16 * e, v);
+              } else {
+                reinterpret_cast<uint4*>(dst + 16 * e)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+                reinterpret_cast<uint4*>(dst + 16 * e)[1] = make_uint4(v[4], v[5], v[6], v[7]);
               }
             }
           }
-          if (issuer) bulk_wait_read<0>();  // before the CTA exits
-        } else if (tok0 < n_tok) {
-          for (int i = 0; i < jobs; ++i) {
-            const int x = i % kBoxesO;
-            const bool resid = i >= kBoxesO;
-            uint32_t oo[64];
-            load_o(x, oo);
-            if (mine) {
-              const Rows& out = resid ? a.resid : a.o;
-              uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out.p) + row * out.ts + head * out.hs + x * 64);
-#pragma unroll
-              for (int cc = 0; cc < 8; ++cc) dst[cc] = pack8(oo + 8 * cc, resid);
-            }
-          }
+          __syncwarp();
         }
-        if (mine) a.lse[static_cast<long long>(head) * a.total + row] = L;
       }
+      if (mine) a.lse[static_cast<long long>(head) * a.total + row] = L;
     }
+    if (issuer) bulk_wait_read<0>();  // a staged box, before the CTA exits
   }
 
   tc_fence_before();
@@ -615,33 +728,31 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, PkCfg<D>::kMinBlocks)
 }
 
 // Merges the parts of the units that were cut along their keys, one warp per
-// row. Grid (KV heads, groups of four rows, units).
+// row. Grid (groups of four rows, cut units).
 template <int D>
 __global__ void __launch_bounds__(128) packed_merge_kernel(const PkArgs a) {
   pdl_wait();
-  if (static_cast<int>(blockIdx.z) >= a.head->splits) return;
+  if (static_cast<int>(blockIdx.y) >= a.head->splits) return;
   constexpr int rows = PkCfg<D>::T * kBM;
-  const PlanSplit sp = a.split_list[blockIdx.z];
+  const PlanSplit sp = a.split_list[blockIdx.y];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rw = blockIdx.y * 4 + warp;
+  const int rw = blockIdx.x * 4 + warp;
   const int t = rw / kBM, rt = rw % kBM;
-  const int kvh = blockIdx.x;
-  const int tok_base = a.cu ? a.cu[sp.seq] : sp.seq;
-  const int n_tok = a.cu ? a.cu[sp.seq + 1] - tok_base : 1;
   const int tok = sp.tok0 + t * a.TT + rt / a.r;
-  if (rt >= a.TT * a.r || tok >= n_tok) return;
-  const int head = kvh * a.r + rt % a.r;
-  const long long row = static_cast<long long>(tok_base) + tok;
-  merge_row<D>(a.part_o, a.part_l, (static_cast<long long>(sp.slot0) * a.Hkv + kvh) * rows + rw,
-               static_cast<long long>(a.Hkv) * rows, sp.parts,
+  if (rt >= a.TT * a.r || tok >= sp.n) return;
+  const int head = sp.kvh * a.r + rt % a.r;
+  const long long row = static_cast<long long>(sp.base) + tok;
+  merge_row<D>(a.part_o, a.part_l, static_cast<long long>(sp.slot0) * rows + rw, rows, sp.parts,
                static_cast<__nv_bfloat16*>(a.o.p) + row * a.o.ts + head * a.o.hs,
                a.lse + static_cast<long long>(head) * a.total + row, lane);
 }
 
 struct Layout {
   PlanLayout plan;
-  int TT, unit, max_splits;
-  long long max_items, max_parts;  // parts: slots * KV heads
+  int TT, unit;
+  bool runs;            // the work may be cut into runs
+  int max_parts;
+  long long max_items;
   size_t off_o, off_l, bytes;
 };
 
@@ -650,25 +761,23 @@ Layout make_layout(const SeqShape& s, const CacheShape* c, int ctas) {
   const int tiles = s.d == 128 ? 2 : 1;
   x.TT = kBM / s.r();
   x.unit = tiles * x.TT;
-  const long long units = plan_max_units(s.S, s.T, x.unit);
-  x.max_items = units;
-  x.max_splits = 0;
-  x.max_parts = 0;
-  // Units are cut only where they are fewer than two per CTA (see plan_kernel).
+  x.max_items = plan_max_units(s.S, s.T, x.unit);
+  // Runs only over a cache, and where there can be so few units (plan_runs()
+  // decides on the device); the cost sums stay in 32 bits.
   const long long least = (static_cast<long long>(s.T) + x.unit - 1) / x.unit;
-  if (c && least * s.Hkv < 2LL * ctas) {
-    const long long tiles_most = (static_cast<long long>(c->max_pages) * c->page + kBN - 1) / kBN;
-    long long parts = units * s.Hkv * ((tiles_most + 3) / 4);
-    if (parts > 4LL * ctas) parts = 4LL * ctas;
-    x.max_parts = parts + s.Hkv;
-    x.max_splits = 2 * ctas / s.Hkv + 1;
-    if (x.max_splits > units) x.max_splits = static_cast<int>(units);
-    x.max_items += 4LL * ctas / s.Hkv + 1;
+  x.runs = c && s.S <= kPlanSeqs && least * s.Hkv < static_cast<long long>(kRunUnits) &&
+           (static_cast<long long>(c->max_pages) * c->page / kBN + 4) * 4 * kRunUnits < (1LL << 31);
+  const int grid = tiles == 2 ? ctas : 2 * ctas;
+  x.max_parts = 0;
+  if (x.runs) {
+    // Each run boundary adds an item and cuts at most one unit.
+    x.max_items += kRunUnits + grid;
+    x.max_parts = 2 * grid;
   }
-  x.plan = plan_layout(x.max_items, x.max_splits);
+  x.plan = plan_layout(x.max_items, x.runs ? grid : 0, x.runs ? grid : 0);
   x.off_o = x.plan.bytes;
   x.off_l = x.off_o + static_cast<size_t>(x.max_parts) * tiles * kBM * s.d * 4;
-  x.bytes = x.off_l + static_cast<size_t>(x.max_parts) * tiles * kBM * 4;
+  x.bytes = x.off_l + static_cast<size_t>(x.max_parts) * tiles * kBM * 4 + 32;  // + alignment of the parts
   return x;
 }
 
@@ -682,16 +791,14 @@ cudaError_t launch_t(const SeqShape& s, const CacheShape* c, const Layout& x, co
   static SmemOnce once;
   cudaError_t e = once.set(reinterpret_cast<const void*>(kern), C::kSmemBytes);
   if (e != cudaSuccess) return e;
-  if constexpr (C::T == 1) {
-    // The register split hands out exactly what a launch at 128 registers
-    // per thread gives the CTA.
-    static const int launch_regs = [&] {
-      cudaFuncAttributes at{};
-      return cudaFuncGetAttributes(&at, kern) == cudaSuccess ? at.numRegs : -1;
-    }();
-    if (launch_regs != 128) return cudaErrorLaunchOutOfResources;
-  }
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  // With another launch count than the split's sum the softmax warps' increase
+  // could never be granted.
+  static const int launch_regs = [&] {
+    cudaFuncAttributes at{};
+    return cudaFuncGetAttributes(&at, kern) == cudaSuccess ? at.numRegs : -1;
+  }();
+  if (launch_regs != C::kLaunchRegs) return cudaErrorLaunchOutOfResources;
+  uint8_t* ws = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(workspace) + 31) / 32 * 32);
   PlanArgs p{};
   p.cu = s.cu;
   p.lens = c ? c->lens : nullptr;
@@ -702,21 +809,20 @@ cudaError_t launch_t(const SeqShape& s, const CacheShape* c, const Layout& x, co
   p.unit = x.unit;
   p.causal = s.causal;
   p.heads = s.Hkv;
-  p.split_ctas = x.max_parts > 0 ? sms : 0;
+  p.run_ctas = x.runs ? C::kMinBlocks * sms : 0;
+  p.half = C::T == 2 ? x.TT : 0;
+  p.run_first = reinterpret_cast<int*>(ws + x.plan.run_first);
   p.sorted = x.max_items * s.Hkv > static_cast<long long>(C::kMinBlocks) * sms;
   p.head = reinterpret_cast<PlanHeader*>(ws + x.plan.head);
   p.items = reinterpret_cast<PlanItem*>(ws + x.plan.items);
-  p.slots = reinterpret_cast<int*>(ws + x.plan.slots);
   p.split_list = reinterpret_cast<PlanSplit*>(ws + x.plan.splits);
   p.err = ctl.err;
   PkArgs a{};
   a.head = p.head;
   a.items = p.items;
-  a.slots = p.slots;
   a.split_list = p.split_list;
-  a.cu = s.cu;
+  a.run_first = p.run_first;
   if (c) {
-    a.lens = c->lens;
     a.table = c->table;
     a.table_stride = c->table_stride;
     a.n_pages = c->n_pages;
@@ -725,6 +831,10 @@ cudaError_t launch_t(const SeqShape& s, const CacheShape* c, const Layout& x, co
   }
   a.o = o;
   a.resid = resid;
+  auto whole = [&](const Rows& y) {
+    return (reinterpret_cast<uintptr_t>(y.p) % 32 == 0) && (s.T == 1 || y.ts % 16 == 0) && (s.Hq == 1 || y.hs % 16 == 0);
+  };
+  a.sectors = whole(o) && (!resid.p || whole(resid));
   a.lse = lse;
   a.part_o = reinterpret_cast<float*>(ws + x.off_o);
   a.part_l = reinterpret_cast<float*>(ws + x.off_l);
@@ -736,14 +846,14 @@ cudaError_t launch_t(const SeqShape& s, const CacheShape* c, const Layout& x, co
   a.scale_log2 = s.scale * 1.4426950408889634f;
   a.rescale_tau = resid.p ? kRescaleExact : kRescaleLazy;
   a.ctl = ctl;
-  const long long grid = x.max_items * s.Hkv;
-  if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  long long grid = x.max_items * s.Hkv;
+  if (x.runs || grid > static_cast<long long>(C::kMinBlocks) * sms) grid = static_cast<long long>(C::kMinBlocks) * sms;
   packed_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   e = launch_dependent(kern, dim3(static_cast<unsigned>(grid)), C::kThreads, C::kSmemBytes, stream, tq, tk, tv, to, tr,
                        a);
-  if (e != cudaSuccess || x.max_splits == 0) return e;
-  return launch_dependent(packed_merge_kernel<D>, dim3(s.Hkv, C::T * kBM / 4, x.max_splits), 128, 0, stream, a);
+  if (e != cudaSuccess || !x.runs) return e;
+  return launch_dependent(packed_merge_kernel<D>, dim3(C::T * kBM / 4, C::kMinBlocks * sms), 128, 0, stream, a);
 }
 
 }  // namespace

@@ -17,13 +17,14 @@ namespace fa {
 struct PlanHeader {
   int items;   // items listed
   int splits;  // units cut along the keys (paged chunks)
-  int pad[2];
+  int taken;   // forward: items taken by the CTAs beyond their first
+  int runs;    // nonzero: CTA c takes items [run_first[c], run_first[c + 1])
 };
 
-// A unit cut along the keys: parts slot0, slot0 + 1, ... of the partial
+// A unit and KV head cut along the keys: parts slot0, slot0 + 1, ... of the partial
 // results, to be merged.
 struct PlanSplit {
-  int seq, tok0, slot0, parts;
+  int base, n, tok0, kvh, slot0, parts;
 };
 
 struct PlanArgs {
@@ -35,29 +36,35 @@ struct PlanArgs {
   int causal;
   int backward;    // items are key tiles of the backward, else query tokens of the forward
   int heads;       // CTAs per item (KV heads)
-  int split_ctas;  // > 0: items may be cut so that this many CTAs are busy
+  int run_ctas;    // > 0: the work may be cut into this many runs
+  int half;        // units of at most this many tokens take less time (0: none)
   int sorted;      // 0: every CTA is resident at once, any order does
   PlanHeader* head;
   PlanItem* items;
-  int* slots;      // per item: its part's slot, -1 when the unit is whole (nullptr: not wanted)
+  int* run_first;
   PlanSplit* split_list;
   unsigned int* err;
 };
 
 constexpr int kPlanSeqs = 1024;    // sequences held in shared memory at a time
 constexpr int kPlanBuckets = 1024;
-// What starting and ending an item costs, in key tiles (partial results of
-// 256 rows written and read again, one CTA's start).
-constexpr float kPlanItemCost = 4.f;
+// Runs are made of fewer units times KV heads than this; more units are
+// balanced well enough by taking them longest first (4 per CTA).
+constexpr int kRunUnits = 4 * 148;
+// Cost of a key tile of a whole unit (two query tiles), of a unit of one query
+// tile, and of starting and ending an item, in quarters of a tile (measured
+// at d = 128: 1.7 us a tile, 4 us an item, part of it beside its neighbours).
+constexpr int kCostTile = 4, kCostHalf = 3, kCostItem = 6;
+// No run end cuts off less than this many key tiles of a unit.
+constexpr int kRunLeast = 3;
 
 struct PlanShared {
   int pre[kPlanSeqs + 1];  // units of the held sequences, summed
-  int n[kPlanSeqs], len[kPlanSeqs];
+  int start[kPlanSeqs], n[kPlanSeqs], len[kPlanSeqs];
   int hist[kPlanBuckets];
   int warp_sum[32];
-  int cand[8];
-  int most, n_splits, n_slots;
-  unsigned int sum;
+  int upos[kRunUnits + 1];  // units' costs, summed
+  int n_splits, n_slots;
 };
 
 // Inclusive sum of `x` over the block of NT threads.
@@ -113,6 +120,7 @@ __device__ void plan_block(const PlanArgs& a, PlanShared& sh) {
         const SeqRange s = seq_range(a.cu, a.lens, b0 + i, a.T, a.max_q, a.max_len);
         bad |= s.bad;
         units = (s.n + a.unit - 1) / a.unit;
+        sh.start[i] = s.start;
         sh.n[i] = s.n;
         sh.len[i] = s.len;
       }
@@ -125,9 +133,9 @@ __device__ void plan_block(const PlanArgs& a, PlanShared& sh) {
     __syncthreads();
     return base;
   };
-  // Unit u of the held sequences: its work (key tiles of the forward, 64-query
-  // steps of the backward).
-  auto unit_of = [&](int b0, int u, int& seq, int& tok0) -> int {
+  // Unit u of the held sequences, as a whole item; returns its work (key
+  // tiles of the forward, 64-query steps of the backward).
+  auto unit_of = [&](int b0, int u, PlanItem& it) -> int {
     int lo = 0, hi = min(kPlanSeqs, a.S - b0) - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -136,12 +144,13 @@ __device__ void plan_block(const PlanArgs& a, PlanShared& sh) {
       else
         hi = mid - 1;
     }
-    seq = b0 + lo;
-    tok0 = (u - sh.pre[lo]) * a.unit;
-    if (a.backward) return (sh.n[lo] + 63) / 64 - (a.causal ? tok0 / 64 : 0);
-    return plan_fwd_tiles(sh.n[lo], sh.len[lo], tok0, a.unit, a.causal);
+    const int n = sh.n[lo], tok0 = (u - sh.pre[lo]) * a.unit;
+    const int w = a.backward ? (n + 63) / 64 - (a.causal ? tok0 / 64 : 0)
+                             : plan_fwd_tiles(n, sh.len[lo], tok0, a.unit, a.causal);
+    it = PlanItem{sh.start[lo], n, sh.len[lo] - n, tok0, 0, w, -1, b0 + lo, -1};
+    return w;
   };
-  // f(u, seq, tok0, work) for every unit.
+  // f(u, item, work) for every unit.
   int held_units = 0;
   auto each = [&](auto f) {
     int base = 0;
@@ -150,17 +159,16 @@ __device__ void plan_block(const PlanArgs& a, PlanShared& sh) {
       const int units = one_chunk ? held_units : load(b0);
 #pragma unroll 1
       for (int u = threadIdx.x; u < units; u += NT) {
-        int seq, tok0;
-        const int w = unit_of(b0, u, seq, tok0);
-        f(base + u, seq, tok0, w);
+        PlanItem it;
+        const int w = unit_of(b0, u, it);
+        f(base + u, it, w);
       }
       base += units;
       if (!one_chunk) __syncthreads();
     }
   };
   for (int i = threadIdx.x; i < kPlanBuckets; i += NT) sh.hist[i] = 0;
-  if (threadIdx.x < 8) sh.cand[threadIdx.x] = 0;
-  if (threadIdx.x == 0) sh.most = sh.n_splits = sh.n_slots = sh.sum = 0;
+  if (threadIdx.x == 0) sh.n_splits = sh.n_slots = 0;
   int U = 0;
   if (one_chunk) {
     U = held_units = load(0);
@@ -176,102 +184,111 @@ __device__ void plan_block(const PlanArgs& a, PlanShared& sh) {
   if (__syncthreads_or(bad)) {
     if (threadIdx.x == 0) {
       atomicOr(a.err, kErrData);
-      *a.head = PlanHeader{0, 0, {0, 0}};
+      *a.head = PlanHeader{0, 0, 0, 0};
     }
     return;
   }
-  if (!a.sorted && a.split_ctas == 0) {
-    each([&](int u, int seq, int tok0, int w) {
-      a.items[u] = PlanItem{seq, tok0, 0, w};
-      if (a.slots) a.slots[u] = -1;
-    });
-    if (threadIdx.x == 0) *a.head = PlanHeader{U, 0, {0, 0}};
-    return;
-  }
-  // Largest work there can be: sets the width of a bucket.
-  long long most = a.backward ? a.T / 64 + 1 : a.max_len / 128 + 1;
-  int L = 0x7fffffff;
-  // Where the units are too few to fill the GPU evenly, cut them along the
-  // keys: the longest length L among eight candidates that gives the least
-  // estimate of the time, (all tiles and starts) / CTAs + half the longest
-  // item, and no less than that item.
-  if (a.split_ctas > 0 && static_cast<long long>(U) * a.heads < 2LL * a.split_ctas) {
-    int my_max = 1;
-    unsigned int my_sum = 0;  // below 2 * 148 units of at most 2^23 tiles: below 2^32
-    each([&](int, int, int, int w) {
-      my_max = max(my_max, w);
-      my_sum += w;
-    });
-    my_max = __reduce_max_sync(0xffffffffu, my_max);
-    my_sum = __reduce_add_sync(0xffffffffu, my_sum);
-    if (lane == 0) {
-      atomicMax(&sh.most, my_max);
-      atomicAdd(&sh.sum, my_sum);
-    }
-    __syncthreads();
-    most = sh.most;
-    const long long all = static_cast<long long>(sh.sum) * a.heads;
-    int len[8], cnt[8];
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      // c = 0: whole units; else about split_ctas * (c + 1) / 4 items.
-      const float l = ceilf(static_cast<float>(all) * 4.f / static_cast<float>(a.split_ctas * (c + 1)));
-      len[c] = c == 0 ? sh.most : static_cast<int>(fminf(fmaxf(l, 4.f), static_cast<float>(sh.most)));
-      cnt[c] = 0;
-    }
-    each([&](int, int, int, int w) {
-#pragma unroll
-      for (int c = 0; c < 8; ++c) cnt[c] += (w + len[c] - 1) / len[c];
-    });
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      const int x = __reduce_add_sync(0xffffffffu, cnt[c]);
-      if (lane == 0 && x) atomicAdd(&sh.cand[c], x);
-    }
-    __syncthreads();
-    float best = 0.f;
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      const float longest = static_cast<float>(len[c]) + kPlanItemCost;
-      const float work = (static_cast<float>(all) + kPlanItemCost * sh.cand[c] * a.heads) / a.split_ctas;
-      const float cost = fmaxf(work + 0.5f * longest, longest);
-      if (c == 0 || cost < best) {
-        best = cost;
-        L = len[c];
+  if (a.run_ctas > 0 && static_cast<long long>(U) * a.heads < kRunUnits) {
+    // Cost of each unit, summed; a run is 1 / run_ctas of all units' and heads'.
+    int total = 0;
+#pragma unroll 1
+    for (int u0 = 0; u0 < U; u0 += NT) {
+      const int u = u0 + threadIdx.x;
+      int cost = 0, sum;
+      if (u < U) {
+        PlanItem it;
+        const int w = unit_of(0, u, it);
+        cost = kCostItem + w * (it.n - it.tok0 <= a.half ? kCostHalf : kCostTile);
       }
+      const int x = plan_scan<NT>(cost, sh.warp_sum, sum);
+      if (u < U) sh.upos[u + 1] = total + x;
+      total += sum;
     }
+    if (threadIdx.x == 0) sh.upos[0] = 0;
+    __syncthreads();
+    const int len = max(1, (total * a.heads + a.run_ctas - 1) / a.run_ctas);
+    // First pass: the runs' sizes; second: the items, from their starts on.
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 1
+      for (int q = threadIdx.x; q < U * a.heads; q += NT) {
+        const int u = q / a.heads;
+        PlanItem it;
+        const int w = unit_of(0, u, it);
+        it.kvh = q - u * a.heads;
+        const int cost = sh.upos[u + 1] - sh.upos[u];
+        const int at = sh.upos[u] * a.heads + it.kvh * cost;
+        const int per = it.n - it.tok0 <= a.half ? kCostHalf : kCostTile;
+        // Key tile at which run r ends within this unit.
+        auto end_tile = [&](int r) {
+          const int x = (r + 1) * len - at;
+          if (x >= cost) return w;
+          const int j = (x - kCostItem) / per;
+          return j < kRunLeast ? 0 : (j > w - kRunLeast ? w : j);
+        };
+        int parts = 0, done = 0;
+#pragma unroll 1
+        for (int r = at / len; done < w; ++r) {
+          const int e = end_tile(r);
+          if (e > done) ++parts;
+          done = max(done, e);
+        }
+        if (pass == 1 && parts > 1) {
+          it.slot = atomicAdd(&sh.n_slots, parts);
+          a.split_list[atomicAdd(&sh.n_splits, 1)] = PlanSplit{it.base, it.n, it.tok0, it.kvh, it.slot, parts};
+        }
+        done = 0;
+#pragma unroll 1
+        for (int r = at / len; done < w; ++r) {
+          const int e = end_tile(r);
+          if (e <= done) continue;
+          const int place = atomicAdd(&sh.hist[r], 1);
+          it.j0 = done;
+          it.j1 = done = e;
+          if (pass == 1) a.items[place] = it;
+          if (parts > 1) ++it.slot;
+        }
+      }
+      __syncthreads();
+      if (pass == 1) break;
+      int run = 0;
+#pragma unroll 1
+      for (int i0 = 0; i0 < a.run_ctas; i0 += NT) {
+        const int i = i0 + threadIdx.x;
+        const int h = i < a.run_ctas ? sh.hist[i] : 0;
+        int sum;
+        const int x = run + plan_scan<NT>(h, sh.warp_sum, sum);
+        if (i < a.run_ctas) {
+          sh.hist[i] = x - h;
+          a.run_first[i + 1] = x;
+        }
+        run += sum;
+      }
+      if (threadIdx.x == 0) a.run_first[0] = 0;
+      __syncthreads();
+    }
+    if (threadIdx.x == 0) *a.head = PlanHeader{U * a.heads, sh.n_splits, 0, 1};
+    return;
   }
+  if (!a.sorted) {
+    each([&](int u, const PlanItem& it, int) { a.items[u] = it; });
+    if (threadIdx.x == 0) *a.head = PlanHeader{U, 0, 0, 0};
+    return;
+  }
+  // Longest first: bucket 0 holds the longest.
+  const long long most = a.backward ? a.T / 64 + 1 : a.max_len / 128 + 1;
   int shift = 0;
   while ((most >> shift) >= kPlanBuckets) ++shift;
-  // Longest first: bucket 0 holds the longest.
-  auto bucket = [&](int w) { return kPlanBuckets - 1 - (w >> shift); };
-  auto parts_of = [&](int w) { return w <= L ? 1 : (w + L - 1) / L; };
   // First pass: the buckets' sizes; second: the items, from their starts on.
-  int run = 0;
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
-    each([&](int, int seq, int tok0, int w) {
-      const int p = parts_of(w);
-      int slot = -1;
-      if (pass == 1 && p > 1) {
-        slot = atomicAdd(&sh.n_slots, p);
-        a.split_list[atomicAdd(&sh.n_splits, 1)] = PlanSplit{seq, tok0, slot, p};
-      }
-      // p parts of nearly equal length: w % p of them one longer.
-      int j = 0;
-#pragma unroll 1
-      for (int k = 0; k < p; ++k) {
-        const int n = p == 1 ? w : w / p + (k < w % p ? 1 : 0);
-        const int at = atomicAdd(&sh.hist[bucket(n)], 1);
-        if (pass == 1) {
-          a.items[at] = PlanItem{seq, tok0, j, j + n};
-          if (a.slots) a.slots[at] = p > 1 ? slot + k : -1;
-        }
-        j += n;
-      }
+    each([&](int, const PlanItem& it, int w) {
+      const int at = atomicAdd(&sh.hist[kPlanBuckets - 1 - (w >> shift)], 1);
+      if (pass == 1) a.items[at] = it;
     });
     __syncthreads();
     if (pass == 1) break;
+    int run = 0;
 #pragma unroll 1
     for (int i0 = 0; i0 < kPlanBuckets; i0 += NT) {
       const int i = i0 + threadIdx.x;
@@ -283,7 +300,12 @@ __device__ void plan_block(const PlanArgs& a, PlanShared& sh) {
     }
     __syncthreads();
   }
-  if (threadIdx.x == 0) *a.head = PlanHeader{run, sh.n_splits, {0, 0}};
+  if (threadIdx.x == 0) *a.head = PlanHeader{U, 0, 0, 0};
+}
+
+__device__ __forceinline__ PlanItem load_item(const PlanItem* p) {
+  const int4 a = reinterpret_cast<const int4*>(p)[0], b = reinterpret_cast<const int4*>(p)[1];
+  return PlanItem{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, p->kvh};
 }
 
 // Largest number of units: sum of ceil(n_b / unit) over S sequences of T
@@ -293,17 +315,17 @@ inline long long plan_max_units(int S, int T, int unit) {
   return most < T ? most : T;
 }
 
-// Bytes of the plan, and its parts' offsets, for at most max_items items.
+// Bytes of the plan, and its parts' offsets.
 struct PlanLayout {
-  size_t head, items, slots, splits, bytes;
+  size_t head, items, run_first, splits, bytes;
 };
-inline PlanLayout plan_layout(long long max_items, int max_splits) {
-  auto up = [](size_t x) { return (x + 15) / 16 * 16; };
+inline PlanLayout plan_layout(long long max_items, int max_runs, int max_splits) {
+  auto up = [](size_t x) { return (x + 31) / 32 * 32; };
   PlanLayout p;
   p.head = 0;
   p.items = up(sizeof(PlanHeader));
-  p.slots = up(p.items + static_cast<size_t>(max_items) * sizeof(PlanItem));
-  p.splits = up(p.slots + static_cast<size_t>(max_items) * 4);
+  p.run_first = up(p.items + static_cast<size_t>(max_items) * sizeof(PlanItem));
+  p.splits = up(p.run_first + (static_cast<size_t>(max_runs) + 1) * 4);
   p.bytes = up(p.splits + static_cast<size_t>(max_splits) * sizeof(PlanSplit));
   return p;
 }
