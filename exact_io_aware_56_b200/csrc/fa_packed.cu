@@ -727,24 +727,74 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, PkCfg<D>::kMinBlocks)
   }
 }
 
-// Merges the parts of the units that were cut along their keys, one warp per
-// row. Grid (groups of four rows, cut units).
+// Merges the parts of the units that were cut along their keys: O = sum_p
+// e^(L_p - L) O_p, L = log sum_p e^(L_p). Mostly two or three parts, so a warp
+// takes kMergeRows rows side by side (a row is one load per lane and part) to
+// keep enough loads in flight (measured at 148 cut units of 256 rows: 16 us
+// with one row per warp). Grid (groups of 4 kMergeRows rows, cut units).
+constexpr int kMergeRows = 4;
 template <int D>
 __global__ void __launch_bounds__(128) packed_merge_kernel(const PkArgs a) {
   pdl_wait();
   if (static_cast<int>(blockIdx.y) >= a.head->splits) return;
   constexpr int rows = PkCfg<D>::T * kBM;
+  constexpr int VW = D / 32;
   const PlanSplit sp = a.split_list[blockIdx.y];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rw = blockIdx.x * 4 + warp;
-  const int t = rw / kBM, rt = rw % kBM;
-  const int tok = sp.tok0 + t * a.TT + rt / a.r;
-  if (rt >= a.TT * a.r || tok >= sp.n) return;
-  const int head = sp.kvh * a.r + rt % a.r;
-  const long long row = static_cast<long long>(sp.base) + tok;
-  merge_row<D>(a.part_o, a.part_l, static_cast<long long>(sp.slot0) * rows + rw, rows, sp.parts,
-               static_cast<__nv_bfloat16*>(a.o.p) + row * a.o.ts + head * a.o.hs,
-               a.lse + static_cast<long long>(head) * a.total + row, lane);
+  const int rw0 = (blockIdx.x * 4 + warp) * kMergeRows;
+  const long long part0 = static_cast<long long>(sp.slot0) * rows + rw0;
+  // Rows of the tile, and of these the ones that hold a token: the others'
+  // partials were never written.
+  bool mine[kMergeRows];
+  int tok[kMergeRows], head[kMergeRows];
+  float acc[kMergeRows][VW], m[kMergeRows], den[kMergeRows];
+#pragma unroll
+  for (int i = 0; i < kMergeRows; ++i) {
+    const int t = (rw0 + i) / kBM, rt = (rw0 + i) % kBM;
+    tok[i] = sp.tok0 + t * a.TT + rt / a.r;
+    head[i] = sp.kvh * a.r + rt % a.r;
+    mine[i] = rt < a.TT * a.r && tok[i] < sp.n;
+    m[i] = -CUDART_INF_F;
+    den[i] = 0.f;
+#pragma unroll
+    for (int k = 0; k < VW; ++k) acc[i][k] = 0.f;
+  }
+#pragma unroll 2
+  for (int p = 0; p < sp.parts; ++p) {
+    float L[kMergeRows], x[kMergeRows][VW];
+#pragma unroll
+    for (int i = 0; i < kMergeRows; ++i) {
+      const long long at = part0 + static_cast<long long>(p) * rows + i;
+      L[i] = mine[i] ? a.part_l[at] : -CUDART_INF_F;
+      if (mine[i])
+        load_vec(a.part_o + at * D + lane * VW, x[i]);
+      else
+#pragma unroll
+        for (int k = 0; k < VW; ++k) x[i][k] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < kMergeRows; ++i) {
+      const float top = fmaxf(m[i], L[i]);
+      const float ref = top == -CUDART_INF_F ? 0.f : top;  // no key so far: every weight 0
+      const float old = expf(m[i] - ref), wt = expf(L[i] - ref);
+      m[i] = top;
+      den[i] = den[i] * old + wt;
+#pragma unroll
+      for (int k = 0; k < VW; ++k) acc[i][k] = acc[i][k] * old + (wt == 0.f ? 0.f : wt * x[i][k]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kMergeRows; ++i) {
+    if (!mine[i]) continue;
+    const float inv = den[i] == 0.f ? 0.f : 1.f / den[i];
+    const long long row = static_cast<long long>(sp.base) + tok[i];
+    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.o.p) + row * a.o.ts + head[i] * a.o.hs +
+                                                lane * VW);
+#pragma unroll
+    for (int k = 0; k < VW / 2; ++k) dst[k] = pack_bf16x2(acc[i][2 * k] * inv, acc[i][2 * k + 1] * inv);
+    if (lane == 0)
+      a.lse[static_cast<long long>(head[i]) * a.total + row] = den[i] == 0.f ? -CUDART_INF_F : m[i] + logf(den[i]);
+  }
 }
 
 struct Layout {
@@ -853,7 +903,7 @@ cudaError_t launch_t(const SeqShape& s, const CacheShape* c, const Layout& x, co
   e = launch_dependent(kern, dim3(static_cast<unsigned>(grid)), C::kThreads, C::kSmemBytes, stream, tq, tk, tv, to, tr,
                        a);
   if (e != cudaSuccess || !x.runs) return e;
-  return launch_dependent(packed_merge_kernel<D>, dim3(C::T * kBM / 4, C::kMinBlocks * sms), 128, 0, stream, a);
+  return launch_dependent(packed_merge_kernel<D>, dim3(C::T * kBM / (4 * kMergeRows), C::kMinBlocks * sms), 128, 0, stream, a);
 }
 
 }  // namespace

@@ -12,7 +12,10 @@
 // angle at p = 10^5 would be off by 4e-3. One block takes a few tokens and
 // computes their cosines and sines once, into shared memory, for all heads;
 // a thread then turns eight pairs of one head per step (two 16-byte loads,
-// two 16-byte stores).
+// two 16-byte stores). Measured at 16384 tokens, 32 + 8 heads, d = 128: 57.6
+// us, 5.8 TB/s (a copy of the same tensors takes 58.1); with 39 registers
+// (six blocks per SM instead of eight) and ordinary accesses 61.8; with four
+// steps' loads ahead of the first store, in 80 registers, 75.
 //
 // The append adds to each token its place len_b - n_b + i in its sequence
 // (found by a 32-way warp search of the offsets), and from the block table
@@ -57,8 +60,9 @@ __device__ __forceinline__ int find_token_seq(const int* cu, int S, int t, int l
   return lo;
 }
 
-__device__ __forceinline__ void load16(const __nv_bfloat16* p, uint4& x) { x = *reinterpret_cast<const uint4*>(p); }
-__device__ __forceinline__ void store16(__nv_bfloat16* p, const uint4& x) { *reinterpret_cast<uint4*>(p) = x; }
+// Streaming (evict-first) accesses: every element passes once.
+__device__ __forceinline__ void load16(const __nv_bfloat16* p, uint4& x) { x = __ldcs(reinterpret_cast<const uint4*>(p)); }
+__device__ __forceinline__ void store16(__nv_bfloat16* p, const uint4& x) { __stcs(reinterpret_cast<uint4*>(p), x); }
 
 // Turns two bf16 pairs held as (a0, a1) in a and (b0, b1) in b.
 __device__ __forceinline__ void turn2(uint32_t& a, uint32_t& b, const float2& t0, const float2& t1) {
@@ -74,7 +78,7 @@ __device__ __forceinline__ void turn1(uint32_t& ab, const float2& t) {
 }
 
 template <bool APPEND>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, 8) rope_kernel(const RopeArgs a) {
   __shared__ float2 turns[kThreads];           // [token][pair]: cos, sin
   __shared__ long long k_at[kMaxTokens];       // page offset of the token's key, -1: none
   __shared__ long long v_at[kMaxTokens];
@@ -157,26 +161,30 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeArgs a) {
       dst = static_cast<__nv_bfloat16*>(a.vp.p) + v_at[i] + h * a.vp.hs;
       rotated = false;
     }
-    rotated = rotated && c * 8 < P;
-    const bool halves = rotated && !a.s.interleaved;
-    const int e0 = halves ? c * 8 : c * 16;
-    const int e1 = halves ? P + c * 8 : c * 16 + 8;
+    // The step's two 16-byte pieces: the halves of eight pairs; or, for
+    // neighbouring pairs and copies, one from each half of the head, so that
+    // neighbouring threads take neighbouring pieces; or, behind pairs that
+    // leave a rest, two of that.
+    const bool halves = rotated && !a.s.interleaved && c * 8 < P;
+    const bool rest = rotated && !a.s.interleaved && !halves;
+    const int e0 = rest ? c * 16 : c * 8;
+    const int e1 = halves ? P + c * 8 : (rest ? c * 16 + 8 : a.s.d / 2 + c * 8);
     uint4 u, w;
     load16(src + e0, u);
     load16(src + e1, w);
-    if (rotated) {
+    uint32_t* pu = reinterpret_cast<uint32_t*>(&u);
+    uint32_t* pw = reinterpret_cast<uint32_t*>(&w);
+    if (halves) {
       const float2* tr = turns + i * P + c * 8;
-      uint32_t* pu = reinterpret_cast<uint32_t*>(&u);
-      uint32_t* pw = reinterpret_cast<uint32_t*>(&w);
-      if (halves) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) turn2(pu[e], pw[e], tr[2 * e], tr[2 * e + 1]);
-      } else {
+      for (int e = 0; e < 4; ++e) turn2(pu[e], pw[e], tr[2 * e], tr[2 * e + 1]);
+    } else if (rotated && !rest) {
+      if (e0 / 2 < P)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) turn1(pu[e], tr[e]);
+        for (int e = 0; e < 4; ++e) turn1(pu[e], turns[i * P + e0 / 2 + e]);
+      if (e1 / 2 < P)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) turn1(pw[e], tr[4 + e]);
-      }
+        for (int e = 0; e < 4; ++e) turn1(pw[e], turns[i * P + e1 / 2 + e]);
     }
     store16(dst + e0, u);
     store16(dst + e1, w);
