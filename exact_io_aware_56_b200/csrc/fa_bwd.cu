@@ -188,52 +188,56 @@ __global__ void __launch_bounds__(kThreads, 1)
   // otherwise small enough that their query heads' Q, dO and dQ-accumulator
   // tiles stay in L2 while the resident CTAs sweep them); within a group the
   // longest units (smallest j when causal) come first.
-  int bkv, j;
+  int bkv = 0, j = 0, r = 1, b = 0, g = 0, i0 = 0, nqi = 0, n_it = 0;
   int base = 0, N = a.N;  // packed: the sequence's first row and its length
   int nq = a.nq;
-  if constexpr (VAR) {
-    static_assert(MASK != 2, "packed sequences: no mask or causal");
-    const int item_no = blockIdx.x / a.Hkv;
-    const PlanItem item = load_item(a.items + item_no);
-    if (item_no >= a.head->items) return;
-    bkv = blockIdx.x - item_no * a.Hkv;
-    j = item.tok0 / kKT;
-    base = item.base;
-    N = item.n;
-    nq = (N + kQT - 1) / kQT;
-  } else if (MASK == 1 && a.band > 0) {
-    // Bands of a.band key tiles, longest band first; within a band,
-    // KV-head-major with the key tiles of a head adjacent, so that the
-    // resident CTAs share the dQ accumulator, Q and dO of a few heads.
-    const int per_band = a.band * a.BHkv;
-    const int band = blockIdx.x / per_band;
-    const int rem = blockIdx.x - band * per_band;
-    const int bw = min(a.band, a.nk - band * a.band);
-    bkv = rem / bw;
-    j = band * a.band + rem % bw;
-  } else {
-    const int per_group = a.group * a.nk;
-    const int grp = blockIdx.x / per_group;
-    const int rem = blockIdx.x - grp * per_group;
-    const int gsize = min(a.group, a.BHkv - grp * a.group);
-    bkv = grp * a.group + rem % gsize;
-    j = rem / gsize;
-  }
-  const int r = a.Hq / a.Hkv;
-  const int b = VAR ? 0 : bkv / a.Hkv;
-  const int g = VAR ? bkv : bkv % a.Hkv;
-  // Query tiles [i0, i0 + nqi) that see some key of tile j: all of them
-  // without a mask or when the tile holds a prefix key; otherwise from the
-  // tile's first key on (causal) up to its last key plus the window.
-  int i0 = 0, i1 = nq;
-  if (MASK == 1) i0 = 2 * j;
-  if (MASK == 2 && j * kKT >= a.prefix) {
-    i0 = 2 * j;
-    const long long last = static_cast<long long>(j) * kKT + kKT - 1 + a.window;
-    i1 = static_cast<int>(min(static_cast<long long>(a.nq), last / kQT + 1));
-  }
-  const int nqi = i1 - i0;             // query tiles per head (the last ends at nq)
-  const int n_it = r * nqi;            // (head, query tile) iterations
+  auto find_unit = [&]() -> bool {
+    if constexpr (VAR) {
+      static_assert(MASK != 2, "packed sequences: no mask or causal");
+      const int item_no = blockIdx.x / a.Hkv;
+      const PlanItem item = load_item(a.items + item_no);
+      if (item_no >= a.head->items) return false;
+      bkv = blockIdx.x - item_no * a.Hkv;
+      j = item.tok0 / kKT;
+      base = item.base;
+      N = item.n;
+      nq = (N + kQT - 1) / kQT;
+    } else if (MASK == 1 && a.band > 0) {
+      // Bands of a.band key tiles, longest band first; within a band,
+      // KV-head-major with the key tiles of a head adjacent, so that the
+      // resident CTAs share the dQ accumulator, Q and dO of a few heads.
+      const int per_band = a.band * a.BHkv;
+      const int band = blockIdx.x / per_band;
+      const int rem = blockIdx.x - band * per_band;
+      const int bw = min(a.band, a.nk - band * a.band);
+      bkv = rem / bw;
+      j = band * a.band + rem % bw;
+    } else {
+      const int per_group = a.group * a.nk;
+      const int grp = blockIdx.x / per_group;
+      const int rem = blockIdx.x - grp * per_group;
+      const int gsize = min(a.group, a.BHkv - grp * a.group);
+      bkv = grp * a.group + rem % gsize;
+      j = rem / gsize;
+    }
+    r = a.Hq / a.Hkv;
+    b = VAR ? 0 : bkv / a.Hkv;
+    g = VAR ? bkv : bkv % a.Hkv;
+    // Query tiles [i0, i0 + nqi) that see some key of tile j: all of them
+    // without a mask or when the tile holds a prefix key; otherwise from the
+    // tile's first key on (causal) up to its last key plus the window.
+    int i1 = nq;
+    if (MASK == 1) i0 = 2 * j;
+    if (MASK == 2 && j * kKT >= a.prefix) {
+      i0 = 2 * j;
+      const long long last = static_cast<long long>(j) * kKT + kKT - 1 + a.window;
+      i1 = static_cast<int>(min(static_cast<long long>(a.nq), last / kQT + 1));
+    }
+    nqi = i1 - i0;             // query tiles per head (the last ends at nq)
+    n_it = r * nqi;            // (head, query tile) iterations
+    return true;
+  };
+  if constexpr (!VAR) find_unit();
 
   if (threadIdx.x == 0) {
     mbar_init(&bars->kv_full, 1);
@@ -267,6 +271,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if constexpr (VAR) {
+    // What is above ran beside the pre-pass, which writes the list and the D_i.
+    pdl_launch_dependents();
+    pdl_wait();
+    if (!find_unit()) {
+      if (warp == kMmaWarp) tmem_dealloc(bars->tmem_base, C::kTmemCols);
+      return;
+    }
+  }
   const uint32_t tmem = bars->tmem_base;
   const Watch w{&bars->abort, a.ctl.err, a.ctl.budget_ns};
 
@@ -857,6 +870,7 @@ template <int D>
 __global__ void __launch_bounds__(kRowThreads)
     packed_pre_kernel(const PlanArgs plan, Rows o, Rows resid, Rows dout, float* __restrict__ dsum,
                       float* __restrict__ dq_acc, const int* __restrict__ cu, int S, int T, int Hq) {
+  pdl_launch_dependents();
   if (blockIdx.x == 0) {
     __shared__ PlanShared sh;
     plan_block<kRowThreads>(plan, sh);
@@ -910,6 +924,7 @@ template <int D>
 __global__ void __launch_bounds__(kRowThreads)
     packed_post_kernel(const float* __restrict__ dq_acc, Rows dq, float scale, const PlanHeader* head,
                        const int* __restrict__ cu, int S, int T, int Hq) {
+  pdl_wait();
   if (head->items == 0) return;
   constexpr int P = D / 8;
   const int t0 = max(0, cu[0]), t1 = min(T, cu[S]);
@@ -1000,10 +1015,11 @@ cudaError_t launch_packed_bwd_t(const SeqShape& s, const PackedBwdLayout& x, con
   a.ctl = ctl;
   const long long grid = x.max_items * s.Hkv;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  kern<<<static_cast<unsigned>(grid), kThreads, C::kSmemBytes, stream>>>(tq, tk, tv, tdo, tdk, tdv, a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  packed_post_kernel<D><<<row_blocks, kRowThreads, 0, stream>>>(dq_acc, dq, s.scale, p.head, s.cu, s.S, s.T, s.Hq);
-  return cudaGetLastError();
+  e = launch_dependent(kern, dim3(static_cast<unsigned>(grid)), kThreads, C::kSmemBytes, stream, tq, tk, tv, tdo, tdk,
+                       tdv, a);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(packed_post_kernel<D>, dim3(row_blocks), kRowThreads, 0, stream, dq_acc, dq, s.scale, p.head,
+                          s.cu, s.S, s.T, s.Hq);
 }
 
 }  // namespace
