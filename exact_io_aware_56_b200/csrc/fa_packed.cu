@@ -307,6 +307,10 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, PkCfg<D>::kMinBlocks)
           int slot = 0, page_no = 0;
           if constexpr (PAGED) page_no = page_of(x, u, slot);
           if (kg >= KS && !(ok = all(wait_bar(&bars->k_empty[s], (kg / KS - 1) & 1, w)))) break;
+          if (a.ctl.fault == 2 && kg == 0) {
+            ok = false;  // test hook: K_0 never arrives
+            break;
+          }
           load_tile(&tmK, &bars->k_full[s], smem + C::kOffK + s * C::kTileBytes, x, u, page_no, slot);
           ++kg;
           if (u > 0) continue;

@@ -295,6 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (g >= ST && !all(wait_bar(&bars->kv_empty[s], (g / ST - 1) & 1, w))) break;
       const uint32_t bytes = static_cast<uint32_t>(parts) * a.pb * 128u * C::kBoxes;
       uint64_t* v_bar = tail ? &bars->v_land[s] : &bars->v_full[s];
+      if (a.ctl.fault == 3) break;  // test hook: K_0 never arrives
       if (lane == 0) {
         mbar_arrive_expect_tx(&bars->k_full[s], bytes);
         mbar_arrive_expect_tx(v_bar, bytes);

@@ -16,6 +16,8 @@
 #include <pybind11/stl.h>
 #include <torch/csrc/utils/pybind.h>
 
+#include <climits>
+#include <cmath>
 #include <optional>
 #include <string>
 #include <vector>
@@ -29,13 +31,19 @@ using Handle = std::optional<uint64_t>;
 
 namespace {
 
-py::object g_error;  // FaError(status, where)
+PyObject* g_error = nullptr;  // the class FaError(status, where); held for good
 
 void done(int rc, const char* where) {
   if (rc == FA_OK) return;
-  py::object e = g_error(rc, where);
-  PyErr_SetObject(g_error.ptr(), e.ptr());
+  py::object e = py::handle(g_error)(rc, where);
+  PyErr_SetObject(g_error, e.ptr());
   throw py::error_already_set();
+}
+
+// A size as the C ABI's int.
+int size32(const char* name, int64_t n) {
+  if (n > INT_MAX || n < INT_MIN) throw py::value_error(std::string(name) + " does not fit 32 bits: " + std::to_string(n));
+  return static_cast<int>(n);
 }
 
 std::string shape_text(at::IntArrayRef s) {
@@ -129,20 +137,20 @@ struct Work {
 struct Seqs {
   int S;
   const int* cu;
-  Seqs(const Opt& t, int64_t T, const Call& c) {
+  Seqs(const Opt& t, int T, const Call& c) {
     if (!t) {
-      S = static_cast<int>(T);
+      S = T;
       cu = nullptr;
       return;
     }
     on_gpu("cu_seqlens", *t);
     if (t->dim() != 1 || t->numel() < 1) throw py::value_error("cu_seqlens must be a tensor of S + 1 offsets");
-    S = static_cast<int>(t->numel() - 1);
+    S = size32("S", t->numel() - 1);
     cu = flat<int>("cu_seqlens", *t, at::kInt, t->sizes(), c);
   }
 };
 
-float scale_of(const std::optional<double>& scale, int64_t d) {
+float scale_of(const std::optional<double>& scale, int d) {
   return static_cast<float>(scale ? *scale : 1.0 / std::sqrt(static_cast<double>(d)));
 }
 
@@ -156,7 +164,8 @@ py::object packed_fwd(const Tensor& q, const Tensor& k, const Tensor& v, const O
   three("q", q);
   three("k", k);
   const Call c(stream);
-  const int64_t T = q.size(0), Hq = q.size(1), Hkv = k.size(1), d = q.size(2);
+  const int T = size32("T", q.size(0)), Hq = size32("Hq", q.size(1)), Hkv = size32("Hkv", k.size(1)),
+            d = size32("d", q.size(2));
   const Seqs s(cu, T, c);
   c.used({&q, &k, &v, &cu, ptr(o_), ptr(lse_), ptr(resid_), ptr(workspace)});
   const Tensor o = out(o_, {T, Hq, d}, q, at::kBFloat16, c);
@@ -182,7 +191,8 @@ py::object packed_bwd(const Tensor& q, const Tensor& k, const Tensor& v, const T
   three("q", q);
   three("k", k);
   const Call c(stream);
-  const int64_t T = q.size(0), Hq = q.size(1), Hkv = k.size(1), d = q.size(2);
+  const int T = size32("T", q.size(0)), Hq = size32("Hq", q.size(1)), Hkv = size32("Hkv", k.size(1)),
+            d = size32("d", q.size(2));
   const Seqs s(cu, T, c);
   c.used({&q, &k, &v, &o, ptr(resid), &dout, &lse, &cu, ptr(dq_), ptr(dk_), ptr(dv_), ptr(workspace)});
   const Tensor dq = out(dq_, {T, Hq, d}, q, at::kBFloat16, c), dk = out(dk_, {T, Hkv, d}, q, at::kBFloat16, c),
@@ -208,7 +218,7 @@ struct Cache {
   const int* table;
   int64_t table_stride;
   const int* lens;
-  Cache(const Tensor& kp, const Tensor& vp, const Tensor& bt, const Tensor& sl, int S, int64_t Hkv, int64_t d,
+  Cache(const Tensor& kp, const Tensor& vp, const Tensor& bt, const Tensor& sl, int S, int Hkv, int d,
         const Call& c) {
     on_gpu("k_pages", kp);
     on_gpu("block_table", bt);
@@ -217,9 +227,9 @@ struct Cache {
     const std::vector<int64_t> shape{kp.size(0), Hkv, kp.size(2), d};
     k = pages("k_pages", kp, shape, c);
     v = pages("v_pages", vp, shape, c);
-    n_pages = static_cast<int>(shape[0]);
-    page = static_cast<int>(shape[2]);
-    max_pages = static_cast<int>(bt.size(1));
+    n_pages = size32("n_pages", shape[0]);
+    page = size32("page_size", shape[2]);
+    max_pages = size32("max_pages", bt.size(1));
     check("block_table", bt, at::kInt, {S, bt.size(1)}, c.dev);
     table = static_cast<const int*>(bt.data_ptr());
     table_stride = bt.stride(0);
@@ -232,11 +242,11 @@ py::object paged_fwd(const Tensor& q, const Tensor& k_pages, const Tensor& v_pag
                      std::optional<double> scale, const Opt& workspace, Handle stream) {
   three("q", q);
   const Call c(stream);
-  const int64_t T = q.size(0), Hq = q.size(1), d = q.size(2);
+  const int T = size32("T", q.size(0)), Hq = size32("Hq", q.size(1)), d = size32("d", q.size(2));
   const Seqs s(cu, T, c);
-  const int64_t Hkv = k_pages.dim() == 4 ? k_pages.size(1) : 0;
+  const int Hkv = k_pages.dim() == 4 ? size32("Hkv", k_pages.size(1)) : 0;
   const Cache ca(k_pages, v_pages, table, lens, s.S, Hkv, d, c);
-  const int64_t mq = max_q ? *max_q : (cu ? std::max<int64_t>(1, T) : 1);
+  const int mq = max_q ? size32("max_q", *max_q) : (cu ? std::max(1, T) : 1);
   c.used({&q, &k_pages, &v_pages, &table, &lens, ptr(cu), ptr(o_), ptr(lse_), ptr(workspace)});
   const Tensor o = out(o_, {T, Hq, d}, q, at::kBFloat16, c);
   const Tensor lse = out(lse_, {Hq, T}, q, at::kFloat, c);
@@ -254,14 +264,14 @@ struct Turn {
   std::vector<int> sections;
   const int* positions = nullptr;
   const double* inv_freq = nullptr;
-  Turn(const Opt& pos, const Opt& freq, const std::optional<std::vector<int>>& sec, int64_t T, const Call& c) {
+  Turn(const Opt& pos, const Opt& freq, const std::optional<std::vector<int>>& sec, int T, const Call& c) {
     if (!freq) {
       if (sec && !sec->empty()) throw py::value_error("sections need inv_freq");
       return;
     }
     on_gpu("inv_freq", *freq);
     const int64_t pairs = freq->numel();
-    sections = sec ? *sec : std::vector<int>{static_cast<int>(pairs)};
+    sections = sec ? *sec : std::vector<int>{size32("pairs", pairs)};
     int64_t sum = 0;
     for (int n : sections) sum += n;
     if (sum != pairs)
@@ -278,7 +288,8 @@ py::object rope(const Opt& q, const Opt& k, const Opt& q_out, const Opt& k_out, 
   if (k) three("k", *k);
   const Call c(stream);
   const Tensor& x = q ? *q : *k;
-  const int64_t T = x.size(0), d = x.size(2), Hq = q ? q->size(1) : 0, Hkv = k ? k->size(1) : 0;
+  const int T = size32("T", x.size(0)), d = size32("d", x.size(2)), Hq = q ? size32("Hq", q->size(1)) : 0,
+            Hkv = k ? size32("Hkv", k->size(1)) : 0;
   const Turn t(pos, freq, sections, T, c);
   c.used({ptr(q), ptr(k), ptr(q_out), ptr(k_out), &pos, &freq});
   fa_rows r[4] = {};
@@ -305,7 +316,8 @@ py::object paged_append(const Opt& q, const Tensor& k, const Tensor& v, const Op
   three("k", k);
   if (q) three("q", *q);
   const Call c(stream);
-  const int64_t T = k.size(0), Hkv = k.size(1), d = k.size(2), Hq = q ? q->size(1) : 0;
+  const int T = size32("T", k.size(0)), Hkv = size32("Hkv", k.size(1)), d = size32("d", k.size(2)),
+            Hq = q ? size32("Hq", q->size(1)) : 0;
   const Seqs s(cu, T, c);
   const Cache ca(k_pages, v_pages, table, lens, s.S, Hkv, d, c);
   const Turn t(pos, freq, sections, T, c);
@@ -328,12 +340,10 @@ py::object paged_append(const Opt& q, const Tensor& k, const Tensor& v, const Op
 }  // namespace
 
 PYBIND11_MODULE(_fa_torch, m) {
-  m.def("set_error", [](py::object e) { g_error = std::move(e); });
+  m.def("set_error", [](py::object e) { g_error = e.release().ptr(); });
   m.def("packed_fwd", &packed_fwd);
   m.def("packed_bwd", &packed_bwd);
   m.def("paged_fwd", &paged_fwd);
   m.def("rope", &rope);
   m.def("paged_append", &paged_append);
-  // Not destroyed at exit, when the interpreter may be gone.
-  m.add_object("_keep", py::capsule(&g_error, [](void*) { g_error.release(); }));
 }

@@ -313,7 +313,10 @@ typedef struct fa_pages {
 
 /*
  * Forward attention over packed sequences: every token attends to its own
- * sequence, causal = 1 to the tokens not behind it.
+ * sequence, causal = 1 to the tokens not behind it. Results repeat bit for
+ * bit. Rows of other sequences may hold anything, NaN included; within a
+ * sequence a key hidden by causality alone has weight 0 in P v, as in
+ * fa_fwd, so that a NaN or infinity in its v reaches earlier rows.
  *   q, o [T][Hq][d], k, v [T][Hkv][d]
  *   o_resid: NULL, or [T][Hq][d], the rounding residual of o (written), as
  *     fa_fwd_with_residual; rounding follows fa_fwd without it and

@@ -9,6 +9,8 @@
  *
  *   code 0: normal operation (default)
  *   code 1: forward producer never loads the first K tile
+ *   code 2: the same in the packed / paged prompt kernel
+ *   code 3: the same in the paged few-row kernel
  *
  * Applies to launches made after the call, from any thread.
  */

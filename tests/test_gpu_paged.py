@@ -38,6 +38,8 @@ FEW = [
     ([7, 25], [40, 2000], 256, 5, 1),           # 125 rows, group of five
     ([1] * 40, [17 + 31 * i for i in range(40)], 8, 4, 4),
     ([128], [128], 16, 1, 1),
+    ([1, 0, 1], [5, 700, 260], 24, 128, 1),     # a group of 128: one token fills the tile
+    ([2, 9], [100, 40], 16, 14, 2),             # groups of seven, 63 rows
 ]
 
 
@@ -56,6 +58,9 @@ CHUNKS = [
     ([257, 1, 1], [400, 2500, 1], 128, 4, 1),
     ([40], [5000], 256, 10, 2),                 # groups of five, few units: cut along the keys
     ([140, 3], [141, 4000], 8, 2, 2),
+    ([2, 3], [400, 1000], 16, 128, 1),          # a group of 128
+    ([70, 1, 9, 2], [1500, 300, 9, 2000], 40, 7, 1),
+    ([130] * 6, [130, 1130, 2130, 700, 300, 1999], 64, 2, 1),
 ]
 
 
@@ -290,4 +295,73 @@ def test_binding_refusals():
     with pytest.raises(fa.FaError) as e:
         call(max_q=0)
     assert e.value.status == fa.FA_ERR_INVALID_ARGUMENT and "fa_paged_fwd" in str(e.value)
+    done()
+
+
+@pytest.mark.parametrize("new,lens", [([1, 1, 1], [300, 5, 1000]), ([150, 3, 40], [700, 3, 1000])])
+@pytest.mark.parametrize("d", [64, 128])
+def test_workspace_contents_do_not_matter(new, lens, d):
+    cache = Cache(97, lens, 16, 2, d)
+    kp, vp, table, ln = cache.cuda()
+    q = normal(98, sum(new), 4, d).cuda()
+    cu = torch.from_numpy(offsets(new)).cuda()
+    n = fa.fa_paged_fwd_workspace_bytes(3, sum(new), max(new), 4, 2, d, 16, table.shape[1])
+    ws = torch.empty(n + 16, dtype=torch.uint8, device="cuda")
+    got = []
+    for fill, at in ((0, 0), (0xFF, 0), (0x7F, 16)):  # NaN and huge patterns, another alignment
+        ws.fill_(fill)
+        got.append(fa.attention_paged(q, kp, vp, table, ln, cu, max(new), True, 0.125, workspace=ws[at:at + n]))
+        done()
+        assert torch.equal(got[-1][0], got[0][0]) and torch.equal(got[-1][1], got[0][1])
+
+
+def test_no_tokens_and_no_sequences():
+    kp = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros(0, 4, 64, dtype=torch.bfloat16, device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    o, lse = fa.attention_paged(q, kp, kp, torch.zeros(0, 3, **i32), torch.zeros(0, **i32))
+    assert o.shape == (0, 4, 64) and lse.shape == (4, 0)
+    o, lse = fa.attention_paged(q, kp, kp, torch.zeros(2, 3, **i32), torch.zeros(2, **i32), torch.zeros(3, **i32), 5)
+    assert o.shape == (0, 4, 64)
+    k = q[:, :2]
+    assert fa.paged_append(k, k, kp, kp, torch.zeros(2, 3, **i32), torch.zeros(2, **i32), torch.zeros(3, **i32), q=q).shape == q.shape
+    fa.attention_packed_forward(q, k, k, torch.zeros(4, **i32), True)
+    done()
+
+
+def test_thousands_of_sequences():
+    # More sequences than a warp sums in one step, some without new tokens or without keys.
+    rng = np.random.default_rng(5)
+    S = 2100
+    new = rng.choice([0, 1, 1, 1, 2], size=S)
+    lens = new + rng.choice([0, 1, 15, 40], size=S)
+    lens[77], lens[1999] = 900, 2300
+    new[77] = new[1999] = 1
+    run([int(x) for x in new], [int(x) for x in lens], 16, 2, 1, 64, seed=3)
+    # ... and through the prompt kernel.
+    new[5] = 140
+    lens[5] = 170
+    run([int(x) for x in new], [int(x) for x in lens], 16, 2, 1, 64, seed=4)
+
+
+def test_two_calls_at_once():
+    # Chunks and single tokens on two streams, each with its own outputs and workspace, beside a packed prompt.
+    a, b = Cache(101, [900, 2000], 16, 2, 64), Cache(102, [3000, 400], 32, 2, 128)
+    da, db = a.cuda(), b.cuda()
+    qa, qb, qp = normal(103, 280, 4, 64).cuda(), normal(104, 2, 8, 128).cuda(), normal(105, 700, 4, 64).cuda()
+    cua, cup = torch.from_numpy(offsets([150, 130])).cuda(), torch.from_numpy(offsets([300, 400])).cuda()
+
+    def calls(streams):
+        return [fa.attention_paged(qa, *da, cua, 150, True, 0.125, stream=streams[0]),
+                fa.attention_paged(qb, *db, scale=0.125, stream=streams[1]),
+                fa.attention_packed_forward(qp, qp[:, :2], qp[:, 2:], cup, True, 0.125, stream=streams[2])]
+
+    want = calls([None] * 3)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for _ in range(20):
+        got = calls(streams)
+        torch.cuda.synchronize()
+        for x, y in zip(got, want):
+            assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
     done()

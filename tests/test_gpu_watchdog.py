@@ -33,3 +33,30 @@ def test_forward_wait_times_out_cleanly_and_context_recovers():
     O, L = oracle.attn_fwd_ref(ref["q"], ref["k"], ref["v"], False, 0.125)
     assert_close_abs("O", to_f64(out), O)
     assert_close_lse(to_f64(l2), L)
+
+
+@pytest.mark.parametrize("code,new,d", [(2, 150, 64), (2, 150, 128), (3, 2, 64), (3, 2, 128)])
+def test_paged_waits_time_out_cleanly_and_context_recovers(code, new, d):
+    import numpy as np
+
+    from .packed import Cache, assert_forward, normal, offsets
+
+    cache = Cache(23, [300, 700], 16, 2, d)
+    kp, vp, table, ln = cache.cuda()
+    q = normal(24, 2 * new, 4, d)
+    args = (q.cuda(), kp, vp, table, ln, torch.from_numpy(offsets([new, new])).cuda(), new, True, 0.125)
+    assert fa.fa_check_device_error() == fa.FA_OK
+    fa.fa_set_watchdog_ns(50_000_000)
+    fa.fa_test_set_fault(code)
+    try:
+        fa.attention_paged(*args)
+        assert fa.fa_check_device_error() == fa.FA_ERR_TIMEOUT
+        assert fa.fa_check_device_error() == fa.FA_OK
+    finally:
+        fa.fa_test_set_fault(0)
+        fa.fa_set_watchdog_ns(2_000_000_000)
+    o, lse = fa.attention_paged(*args)
+    torch.cuda.synchronize()
+    assert fa.fa_check_device_error() == fa.FA_OK
+    assert_forward(o, lse, *oracle.paged_ref(to_f64(q), to_f64(cache.k), to_f64(cache.v), cache.table,
+                                             np.asarray(cache.lens), offsets([new, new]), True, 0.125))
