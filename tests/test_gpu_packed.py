@@ -230,3 +230,74 @@ def test_many_sequences():
     done()
     assert_forward(o, lse, *oracle.packed_fwd_ref(to_f64(q), to_f64(k), to_f64(v), cu, True, 0.125))
     backward_check(q, k, v, dout, g, cu, True, 0.125)
+
+
+def weight_error(q, k, scale):
+    """Relative error of a weight for scores of any size: half a bf16 step, plus the error of its exponent: S in fp32
+    over d products (d 2^-24 of the sum of their magnitudes), L's own error of that size, 1.2e-4 each for the
+    exponential and the row sum."""
+    d = q.shape[-1]
+    most = scale * float(np.abs(to_f64(q)).max(0).max(0) @ np.abs(to_f64(k)).max(0).max(0))
+    return HALF + 2 * (d * 2.0 ** -24 * most + 1.2e-4)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("d", [64, 128])
+def test_large_and_rising_scores(d, causal):
+    # Peaky rows: q, k three times as large, and keys that rise along the sequence, so that a row's max keeps growing
+    # by less and by more than the forward's rescale threshold.
+    lens, hq, hkv = [700, 300], 4, 2
+    q, k, v, dout = inputs(lens, hq, hkv, d, 141)
+    u = normal(142, 1, 1, d).float()
+    u = u / u.norm()
+    rise = torch.cat([torch.linspace(0, 60, n) for n in lens])[:, None, None]
+    q = (2 * q.float() + 4 * u).to(torch.bfloat16)
+    k = (2 * k.float() + rise * u).to(torch.bfloat16)
+    cu = offsets(lens)
+    cud = torch.from_numpy(cu).cuda()
+    scale = d ** -0.5
+    w = weight_error(q, k, scale)
+    O, L, A = oracle.packed_fwd_ref(to_f64(q), to_f64(k), to_f64(v), cu, causal, scale)
+    for residual in (False, True):
+        got = fa.attention_packed_forward(q.cuda(), k.cuda(), v.cuda(), cud, causal, scale, residual=residual)
+        done()
+        assert_within("O", got[0], O, w * A + HALF * np.abs(O) + 1e-6)
+        assert_within("L", got[1], L, (w - HALF) + 2.0 ** -22 * np.abs(L))
+    grads = fa.attention_packed_backward(q.cuda(), k.cuda(), v.cuda(), got[0], dout.cuda(), got[1], cud, causal, scale,
+                                         o_resid=got[2])
+    done()
+    ref = oracle.packed_bwd_ref(*(to_f64(x) for x in (q, k, v, dout)), cu, causal, scale, w)
+    for got_, want, err in zip(grads, ref[:3], ref[3:]):
+        assert_within("gradient", got_, want, err + HALF * np.abs(want) + 1e-4)
+
+
+def test_saturated_rows_are_exact():
+    # One key carries all of a row's weight: O = v of that key, bit for bit, and dQ = dK = 0.
+    lens, hq, hkv, d = [200, 129, 1], 4, 2, 64
+    T = sum(lens)
+    g = torch.Generator().manual_seed(5)
+    k = (torch.randint(0, 2, (T, hkv, d), generator=g) * 2 - 1).to(torch.bfloat16)
+    v, dout = normal(6, T, hkv, d), normal(7, T, hq, d)
+    cu = offsets(lens)
+    rng = np.random.default_rng(5)
+    pick = np.zeros((T, hq), dtype=np.int64)
+    for b in range(3):
+        for t in range(cu[b], cu[b + 1]):
+            pick[t] = rng.integers(cu[b], t + 1, size=hq)
+    heads = np.arange(hq) // 2
+    q = 64 * k[torch.from_numpy(pick), torch.from_numpy(heads)[None]]
+    kf = to_f64(k)
+    for b in range(3):  # every other visible key is far below
+        for t in range(cu[b], cu[b + 1]):
+            for h in range(hq):
+                dots = kf[cu[b]:t + 1, heads[h]] @ kf[pick[t, h], heads[h]]
+                dots[pick[t, h] - cu[b]] = -1e9
+                assert 64 * 0.125 * np.log2(np.e) * (d - dots.max()) > 160
+    cud = torch.from_numpy(cu).cuda()
+    o, lse, r = fa.attention_packed_forward(q.cuda(), k.cuda(), v.cuda(), cud, True, 0.125, residual=True)
+    dq, dk, dv = fa.attention_packed_backward(q.cuda(), k.cuda(), v.cuda(), o, dout.cuda(), lse, cud, True, 0.125,
+                                              o_resid=r)
+    done()
+    assert torch.equal(o.cpu(), v[torch.from_numpy(pick), torch.from_numpy(heads)[None]])
+    assert (lse.cpu().t() / (0.125 * 64 * d) - 1).abs().max() < 2e-6
+    assert (r == 0).all()

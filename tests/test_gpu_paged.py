@@ -365,3 +365,29 @@ def test_two_calls_at_once():
         for x, y in zip(got, want):
             assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
     done()
+
+
+@pytest.mark.parametrize("new", [[1, 3], [200, 9]])
+@pytest.mark.parametrize("d", [64, 128])
+def test_large_and_rising_scores(new, d):
+    from .packed import HALF, assert_within
+    from .test_gpu_packed import weight_error
+
+    lens, hq, hkv, page = [900, 2000], 8, 2, 16
+    cache = Cache(111, lens, page, hkv, d)
+    u = normal(112, 1, 1, 1, d).float()
+    u = u / u.norm()
+    for b, n in enumerate(lens):
+        for j in range(-(-n // page)):
+            p = cache.table[b, j]
+            cache.k[p] = (2 * cache.k[p].float() + 60.0 * j * page / n * u[0]).to(torch.bfloat16)
+    q = (2 * normal(113, sum(new), hq, d).float() + 4 * u[0]).to(torch.bfloat16)
+    kp, vp, table, ln = cache.cuda()
+    cu = offsets(new)
+    scale = d ** -0.5
+    o, lse = fa.attention_paged(q.cuda(), kp, vp, table, ln, torch.from_numpy(cu).cuda(), max(new), True, scale)
+    done()
+    O, L, A = oracle.paged_ref(to_f64(q), to_f64(cache.k), to_f64(cache.v), cache.table, cache.lens, cu, True, scale)
+    w = weight_error(q, cache.k.nan_to_num(0.0).flatten(0, 1).flatten(0, 1)[:, None], scale)
+    assert_within("O", o, O, w * A + HALF * np.abs(O) + 1e-6)
+    assert_within("L", lse, L, (w - HALF) + 2.0 ** -22 * np.abs(L))
