@@ -569,11 +569,12 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, PkCfg<D>::kMinBlocks)
               float x0, x1;
               ffma2(x0, x1, __uint_as_float(sr[b * 32 + 2 * e]), __uint_as_float(sr[b * 32 + 2 * e + 1]), sl2, sl2,
                     neg_m, neg_m);
-              // Shares of the FMA pipe as in fa_fwd.cu (2 of 32 at d = 128,
-              // none at d = 64 causal).
-              constexpr int kPoly = D == 128 ? 2 : 0;
-              const float p0 = (2 * e < kPoly) ? exp2_poly(x0) : ex2(x0);
-              const float p1 = (2 * e + 1 < kPoly) ? exp2_poly(x1) : ex2(x1);
+              // All on the exponential unit: two of 32 on the FMA pipe, as in
+              // fa_fwd.cu at d = 128, gained nothing here (678-685 us against
+              // 672-679 at 16k packed tokens), and their error (1e-4) would
+              // enter L.
+              const float p0 = ex2(x0);
+              const float p1 = ex2(x1);
               fadd2(ps[(2 * e) & 7], ps[(2 * e + 1) & 7], ps[(2 * e) & 7], ps[(2 * e + 1) & 7], p0, p1);
               // bf16: the type of V, which the weights meet in P V.
               pk[e] = pack_bf16x2(p0, p1);

@@ -143,7 +143,8 @@ def test_agrees_with_the_equal_length_kernels(d):
     done()
     # Each is within W sum P|v| + 2^-8 |O| of the same exact value, and sum P|v| <= max |v|.
     assert (batch(o).float() - ob.float()).abs().max() <= 2 * (W + HALF) * v.float().abs().max()
-    assert (lse.unflatten(1, (2, 256)).transpose(0, 1) - lb).abs().max() <= 2 * TOL_L
+    # (The equal-length kernel evaluates some exponentials by a polynomial of relative error 1.2e-4.)
+    assert (lse.unflatten(1, (2, 256)).transpose(0, 1) - lb).abs().max() <= 2 * TOL_L + 1.2e-4
     backward_check(*(x.cpu() for x in (q, k, v, dout)), g, np.array([0, 256, 512]), True, d ** -0.5)
     backward_check(*(x.cpu() for x in (q, k, v, dout)), [x.transpose(1, 2).flatten(0, 1) for x in gb],
                    np.array([0, 256, 512]), True, d ** -0.5)
@@ -234,8 +235,8 @@ def test_many_sequences():
 
 def weight_error(q, k, scale):
     """Relative error of a weight for scores of any size: half a bf16 step, plus the error of its exponent: S in fp32
-    over d products (d 2^-24 of the sum of their magnitudes), L's own error of that size, 1.2e-4 each for the
-    exponential and the row sum."""
+    over d products (d 2^-24 of the sum of their magnitudes), L's own error of that size, and 1.2e-4 each for the
+    exponentials and for fp32 of large exponents."""
     d = q.shape[-1]
     most = scale * float(np.abs(to_f64(q)).max(0).max(0) @ np.abs(to_f64(k)).max(0).max(0))
     return HALF + 2 * (d * 2.0 ** -24 * most + 1.2e-4)
