@@ -37,7 +37,10 @@
 // holds the next sequence's rows, which may be anything: warp 10 zeroes them
 // in shared memory (K, V once; Q and dO of each head's last tile), after
 // which they are what rows past N are to the equal-length form, where TMA
-// fills zeros. dK and dV of such a tile are stored row by row.
+// fills zeros. dK and dV of such a tile are stored row by row. Fewer units
+// than SMs (few KV heads, short packs) are cut into parts of their (head,
+// query tile) iterations, whose dK and dV are added up in fp32 and converted
+// by the last kernel.
 //
 // Warp roles of bwd_main (512 threads):
 //   warps 0-3   softmax-gradient warpgroup for even query tiles (buffer 0),
@@ -121,6 +124,7 @@ struct BwdArgs {
   const PlanHeader* head;
   const PlanItem* items;
   Rows dk, dv;
+  float *dk_acc, *dv_acc;  // fp32 [Hkv][T][d], for units cut into parts
   LaunchCtl ctl;
 };
 
@@ -142,6 +146,16 @@ __device__ __forceinline__ void fence_async_smem() {
 
 __device__ __forceinline__ void red_add_f32(float* addr, float v) {
   asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(addr), "f"(v) : "memory");
+}
+
+// Adds 32 columns of a row, times f, to an fp32 accumulator (16-byte aligned).
+__device__ __forceinline__ void add_row32(float* dst, const uint32_t (&v)[32], float f) {
+#pragma unroll
+  for (int e = 0; e < 32; e += 4)
+    asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(dst + e),
+                 "f"(__uint_as_float(v[e]) * f), "f"(__uint_as_float(v[e + 1]) * f), "f"(__uint_as_float(v[e + 2]) * f),
+                 "f"(__uint_as_float(v[e + 3]) * f)
+                 : "memory");
 }
 
 // Stores `rows` rows of a staged tile (64-column boxes of 128-byte rows,
@@ -189,6 +203,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // tiles stay in L2 while the resident CTAs sweep them); within a group the
   // longest units (smallest j when causal) come first.
   int bkv = 0, j = 0, r = 1, b = 0, g = 0, i0 = 0, nqi = 0, n_it = 0;
+  int it0 = 0;        // packed: first iteration of this part of the unit
+  bool parts = false;  // packed: the unit is one of several parts
   int base = 0, N = a.N;  // packed: the sequence's first row and its length
   int nq = a.nq;
   auto find_unit = [&]() -> bool {
@@ -202,6 +218,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       base = item.base;
       N = item.n;
       nq = (N + kQT - 1) / kQT;
+      it0 = item.j0;
+      n_it = item.j1 - item.j0;
+      parts = a.head->runs != 0;
     } else if (MASK == 1 && a.band > 0) {
       // Bands of a.band key tiles, longest band first; within a band,
       // KV-head-major with the key tiles of a head adjacent, so that the
@@ -234,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       i1 = static_cast<int>(min(static_cast<long long>(a.nq), last / kQT + 1));
     }
     nqi = i1 - i0;             // query tiles per head (the last ends at nq)
-    n_it = r * nqi;            // (head, query tile) iterations
+    if (!VAR) n_it = r * nqi;  // (head, query tile) iterations
     return true;
   };
   if constexpr (!VAR) find_unit();
@@ -321,8 +340,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xffffffffu, wait_bar(&bars->q_empty[s], (u - 1) & 1, w));
         if (!ok) break;
       }
-      const int h = g * r + it / nqi;
-      const int i = i0 + it % nqi;
+      const int h = g * r + (it0 + it) / nqi;
+      const int i = i0 + (it0 + it) % nqi;
       const int bh = b * a.Hq + h;
       // L (in log2 units) and D for the 64 query rows of this tile; rows
       // past N get L = +inf so that their P is exactly 0.
@@ -381,11 +400,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&bars->kv_full);
       }
     }
-    // The last query tile of each head, when it is short: iterations
-    // nqi - 1, 2 nqi - 1, ...
+    // The last query tile of each head, when it is short: every nqi-th
+    // iteration of the unit.
     if (nq * kQT > N) {
       uint32_t land_par = 0;
-      for (int it = nqi - 1; ok && it < n_it; it += nqi) {
+      for (int it = nqi - 1 - it0 % nqi; ok && it < n_it; it += nqi) {
         const int s = it % kQStages;
         ok = __all_sync(0xffffffffu, wait_bar(&bars->q_land[s], (land_par >> s) & 1, w));
         if (!ok) break;
@@ -508,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int it = x; it < n_it; it += 2) {
       const int s = it % kQStages;
-      const int i = i0 + it % nqi;
+      const int i = i0 + (it0 + it) % nqi;
       const uint32_t par = (it >> 1) & 1;
       const float* l2 = sLD + s * 2 * kQT;
       const float* dd = l2 + kQT;
@@ -609,6 +628,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int c = x * (D / 64) + cc;  // 32-column chunk
         uint32_t vv[32];
         tmem_ld32(tmem + lane_off + C::kColDV + c * 32, vv);
+        if (VAR && parts) {
+          if (j * kKT + kr < N)
+            add_row32(a.dv_acc + ((static_cast<long long>(bkv) * a.N + base + j * kKT + kr) * D + c * 32), vv, 1.f);
+          __syncwarp();
+          continue;
+        }
         uint8_t* row = smem + C::kOffV + (c / 2) * C::kKBox + kr * 128;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
@@ -622,7 +647,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       fence_proxy_async_smem();
       mbar_arrive(&bars->epi_dv);
-      if (VAR && (j + 1) * kKT > N) {
+      if (VAR && parts) {
+      } else if (VAR && (j + 1) * kKT > N) {
         // The tile's rows of this sequence, from the staged boxes, 16 bytes
         // per thread and step.
         if (__all_sync(0xffffffffu, wait_bar(&bars->epi_dv, 0, w)))
@@ -650,8 +676,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __all_sync(0xffffffffu, wait_bar(&bars->dq_full[x], (it >> 1) & 1, w));
       if (!ok) break;
       tc_fence_after();
-      const int h = g * r + it / nqi;
-      const int i = i0 + it % nqi;
+      const int h = g * r + (it0 + it) / nqi;
+      const int i = i0 + (it0 + it) % nqi;
       const int bh = b * a.Hq + h;
       uint32_t v0[32], v1[32];
       const uint32_t tDQ = tmem + lane_off + C::kColDP + 64 * x;
@@ -687,6 +713,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < D / 32; ++c) {
         uint32_t vv[32];
         tmem_ld32(tmem + lane_off + C::kColDK + c * 32, vv);
+        if (VAR && parts) {
+          if (j * kKT + m < N)
+            add_row32(a.dk_acc + ((static_cast<long long>(bkv) * a.N + base + j * kKT + m) * D + c * 32), vv, a.scale);
+          __syncwarp();
+          continue;
+        }
         uint8_t* row = smem + C::kOffK + (c / 2) * C::kKBox + m * 128;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
@@ -701,7 +733,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_proxy_async_smem();
       mbar_arrive(&bars->epi_dk);
       const bool issuer = warp == kDqWarp0 && lane == 0;
-      if (VAR && (j + 1) * kKT > N) {
+      if (VAR && parts) {
+      } else if (VAR && (j + 1) * kKT > N) {
         if (__all_sync(0xffffffffu, wait_bar(&bars->epi_dk, 0, w)))
           store_rows_t<D>(smem + C::kOffK, C::kKBox, N - j * kKT, a.dk, base + j * kKT, bkv, m, 128);
       } else if (issuer && wait_bar(&bars->epi_dk, 0, w)) {
@@ -869,13 +902,18 @@ struct RowPieces {
 template <int D>
 __global__ void __launch_bounds__(kRowThreads)
     packed_pre_kernel(const PlanArgs plan, Rows o, Rows resid, Rows dout, float* __restrict__ dsum,
-                      float* __restrict__ dq_acc, const int* __restrict__ cu, int S, int T, int Hq) {
+                      float* __restrict__ dq_acc, float4* __restrict__ kv_acc, long long kv_pieces,
+                      const int* __restrict__ cu, int S, int T, int Hq) {
   pdl_launch_dependents();
   if (blockIdx.x == 0) {
     __shared__ PlanShared sh;
     plan_block<kRowThreads>(plan, sh);
     return;
   }
+  // (The dK and dV accumulators of units that may be cut into parts.)
+  for (long long e = static_cast<long long>(blockIdx.x - 1) * kRowThreads + threadIdx.x; e < kv_pieces;
+       e += static_cast<long long>(gridDim.x - 1) * kRowThreads)
+    kv_acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
   constexpr int P = D / 8;  // lanes per row
   const int t0 = max(0, cu[0]), t1 = min(T, cu[S]);
   const int items = Hq * P;
@@ -918,50 +956,73 @@ __global__ void __launch_bounds__(kRowThreads)
   }
 }
 
-// dq = bf16(scale * accumulator) for the packed rows, 8 elements per thread
-// and step; nothing when the plan found the offsets out of range.
+// out = bf16(f * accumulator) for rows [t0, t1) of H heads, 8 elements per
+// thread and step; acc is [H][T][D].
 template <int D>
-__global__ void __launch_bounds__(kRowThreads)
-    packed_post_kernel(const float* __restrict__ dq_acc, Rows dq, float scale, const PlanHeader* head,
-                       const int* __restrict__ cu, int S, int T, int Hq) {
-  pdl_wait();
-  if (head->items == 0) return;
+__device__ __forceinline__ void convert_rows(const float* __restrict__ acc, const Rows& out, float f, int t0, int t1, int T,
+                                             int H) {
   constexpr int P = D / 8;
-  const int t0 = max(0, cu[0]), t1 = min(T, cu[S]);
-  const int items = Hq * P;
+  const int items = H * P;
   const RowPieces my(items);
   if (my.sub >= my.tpb) return;
   for (long long t = t0 + static_cast<long long>(blockIdx.x) * my.tpb + my.sub; t < t1;
        t += static_cast<long long>(gridDim.x) * my.tpb) {
     for (int i = my.first; i < items; i += my.step) {
       const int h = i / P, c = i % P;
-      const float4* src = reinterpret_cast<const float4*>(dq_acc + (static_cast<long long>(h) * T + t) * D + c * 8);
+      const float4* src = reinterpret_cast<const float4*>(acc + (static_cast<long long>(h) * T + t) * D + c * 8);
       const float4 x = src[0], y = src[1];
-      uint4 out;
-      out.x = pack_bf16x2(x.x * scale, x.y * scale);
-      out.y = pack_bf16x2(x.z * scale, x.w * scale);
-      out.z = pack_bf16x2(y.x * scale, y.y * scale);
-      out.w = pack_bf16x2(y.z * scale, y.w * scale);
-      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(dq.p) + t * dq.ts + h * dq.hs + c * 8) = out;
+      uint4 v;
+      v.x = pack_bf16x2(x.x * f, x.y * f);
+      v.y = pack_bf16x2(x.z * f, x.w * f);
+      v.z = pack_bf16x2(y.x * f, y.y * f);
+      v.w = pack_bf16x2(y.z * f, y.w * f);
+      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out.p) + t * out.ts + h * out.hs + c * 8) = v;
     }
   }
 }
 
+// dq, and dk and dv of units that were cut into parts, from their
+// accumulators; nothing when the plan found the offsets out of range.
+template <int D>
+__global__ void __launch_bounds__(kRowThreads)
+    packed_post_kernel(const float* __restrict__ dq_acc, Rows dq, float scale, const float* __restrict__ dk_acc, Rows dk,
+                       const float* __restrict__ dv_acc, Rows dv, const PlanHeader* head, const int* __restrict__ cu, int S,
+                       int T, int Hq, int Hkv) {
+  pdl_wait();
+  if (head->items == 0) return;
+  const int t0 = max(0, cu[0]), t1 = min(T, cu[S]);
+  convert_rows<D>(dq_acc, dq, scale, t0, t1, T, Hq);
+  if (head->runs) {
+    convert_rows<D>(dk_acc, dk, 1.f, t0, t1, T, Hkv);
+    convert_rows<D>(dv_acc, dv, 1.f, t0, t1, T, Hkv);
+  }
+}
+
+constexpr int kPartCtas = 148;  // one CTA per SM
+
 struct PackedBwdLayout {
   PlanLayout plan;
   long long max_items;
-  size_t off_d, off_dq, bytes;
+  bool parts;  // units may be cut into parts
+  size_t off_d, off_dq, off_dk, off_dv, bytes;
 };
 
 PackedBwdLayout packed_bwd_layout(const SeqShape& s) {
   PackedBwdLayout x;
   x.max_items = plan_max_units(s.S, s.T, kKT);
+  // Where there can be fewer units than CTAs; a KV head's share of the CTAs
+  // bounds its parts.
+  x.parts = (static_cast<long long>(s.T) + kKT - 1) / kKT * s.Hkv < kPartCtas;
+  if (x.parts) x.max_items += kPartCtas;
   x.plan = plan_layout(x.max_items, 0, 0);
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   x.off_d = up(x.plan.bytes);
   const size_t rows = static_cast<size_t>(s.T) * s.Hq;
   x.off_dq = up(x.off_d + rows * 4);
-  x.bytes = x.off_dq + rows * s.d * 4;
+  x.off_dk = up(x.off_dq + rows * s.d * 4);
+  const size_t kv = x.parts ? static_cast<size_t>(s.T) * s.Hkv * s.d * 4 : 0;
+  x.off_dv = x.off_dk + kv;
+  x.bytes = x.off_dv + kv;
   return x;
 }
 
@@ -989,14 +1050,19 @@ cudaError_t launch_packed_bwd_t(const SeqShape& s, const PackedBwdLayout& x, con
   p.causal = s.causal;
   p.backward = 1;
   p.heads = s.Hkv;
-  p.sorted = x.max_items * s.Hkv > 148;
+  p.sorted = 1;
+  p.r = s.r();
+  p.part_ctas = x.parts ? kPartCtas : 0;
   p.head = reinterpret_cast<PlanHeader*>(ws + x.plan.head);
   p.items = reinterpret_cast<PlanItem*>(ws + x.plan.items);
   p.err = ctl.err;
   const long long rows = static_cast<long long>(s.T) * s.Hq;
   const int row_blocks = grid_for(rows * (D / 8), kRowThreads, 148 * 64);
-  packed_pre_kernel<D><<<1 + row_blocks, kRowThreads, 0, stream>>>(p, o, resid, dout, dsum, dq_acc, s.cu, s.S, s.T,
-                                                                   s.Hq);
+  float* dk_acc = x.parts ? reinterpret_cast<float*>(ws + x.off_dk) : nullptr;
+  float* dv_acc = x.parts ? reinterpret_cast<float*>(ws + x.off_dv) : nullptr;
+  packed_pre_kernel<D><<<1 + row_blocks, kRowThreads, 0, stream>>>(
+      p, o, resid, dout, dsum, dq_acc, reinterpret_cast<float4*>(dk_acc), static_cast<long long>(x.bytes - x.off_dk) / 16,
+      s.cu, s.S, s.T, s.Hq);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   BwdArgs a{};
   a.lse = lse;
@@ -1012,14 +1078,16 @@ cudaError_t launch_packed_bwd_t(const SeqShape& s, const PackedBwdLayout& x, con
   a.items = p.items;
   a.dk = dk;
   a.dv = dv;
+  a.dk_acc = dk_acc;
+  a.dv_acc = dv_acc;
   a.ctl = ctl;
   const long long grid = x.max_items * s.Hkv;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   e = launch_dependent(kern, dim3(static_cast<unsigned>(grid)), kThreads, C::kSmemBytes, stream, tq, tk, tv, tdo, tdk,
                        tdv, a);
   if (e != cudaSuccess) return e;
-  return launch_dependent(packed_post_kernel<D>, dim3(row_blocks), kRowThreads, 0, stream, dq_acc, dq, s.scale, p.head,
-                          s.cu, s.S, s.T, s.Hq);
+  return launch_dependent(packed_post_kernel<D>, dim3(row_blocks), kRowThreads, 0, stream, dq_acc, dq, s.scale, dk_acc, dk,
+                          dv_acc, dv, p.head, s.cu, s.S, s.T, s.Hq, s.Hkv);
 }
 
 }  // namespace

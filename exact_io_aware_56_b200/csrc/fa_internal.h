@@ -221,7 +221,7 @@ struct alignas(16) PlanItem {
   int base, n;   // the sequence's first row and its tokens
   int off;       // place of its first token (paged), else 0
   int tok0;      // first token of the item
-  int j0, j1;    // forward: key tiles; backward: [0, steps)
+  int j0, j1;    // forward: key tiles; backward: (head, query tile) steps
   int slot;      // part of a unit cut along its keys, -1: whole unit
   int seq;
   int kvh;       // KV head, where the items carry it

@@ -20,9 +20,9 @@
 //    resident and take items until none is left; the next item's first K/V
 //    tiles and Q load, and its first S products run, beside this one's last
 //    softmax and epilogue. (One CTA per item spent 5.9 us of 44 per item on
-//    starting, first loads and ending, at 16k packed tokens, d = 128.) Chunks
-//    over a cache that make too few units to fill the GPU evenly are instead
-//    cut into one run per CTA of equal cost; units that a run's end cuts along
+//    starting, first loads and ending, at 16k packed tokens, d = 128.) Too
+//    few units to fill the GPU evenly (chunks over a long cache, few heads) are
+//    instead cut into one run per CTA of equal cost; units that a run's end cuts along
 //    their keys leave O / l and logsumexp in the workspace and a second kernel
 //    merges them.
 //  * Tiles end where sequences do: scores of keys behind the end are replaced
@@ -165,7 +165,9 @@ __device__ __forceinline__ Unit make_unit(const PlanItem& it, int kvh, int TT, i
   return x;
 }
 
-template <int D, bool PAGED>
+// RUNS: the work may be cut into runs, and units into parts. (Without, the
+// kernel has no path for partial results: 1% at 16k packed tokens.)
+template <int D, bool PAGED, bool RUNS>
 __global__ void __launch_bounds__(PkCfg<D>::kThreads, PkCfg<D>::kMinBlocks)
     packed_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
@@ -280,7 +282,7 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, PkCfg<D>::kMinBlocks)
       }
       // Items of the list times the KV heads, taken one by one; or, where the
       // plan cut the work into runs, this CTA's own items.
-      const bool runs = a.head->runs != 0;
+      const bool runs = RUNS && a.head->runs != 0;
       int idx = runs ? a.run_first[blockIdx.x] : blockIdx.x;
       const int total = runs ? a.run_first[blockIdx.x + 1] : a.head->items * a.Hkv;
       int kg = 0, q_uses[2] = {0, 0};
@@ -631,7 +633,7 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, PkCfg<D>::kMinBlocks)
 #pragma unroll
         for (int e = 0; e < 64; ++e) oo[e] = __float_as_uint(__uint_as_float(oo[e]) * inv_l);
       };
-      if (PAGED && x.it.slot >= 0) {
+      if (RUNS && x.it.slot >= 0) {
         const long long prow = static_cast<long long>(x.it.slot) * (T * kBM) + t * kBM + rw;
 #pragma unroll
         for (int b = 0; b < D / 64; ++b) {
@@ -733,72 +735,124 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, PkCfg<D>::kMinBlocks)
 }
 
 // Merges the parts of the units that were cut along their keys: O = sum_p
-// e^(L_p - L) O_p, L = log sum_p e^(L_p). Mostly two or three parts, so a warp
+// e^(L_p - L) O_p, L = log sum_p e^(L_p). Mostly two or three parts: a warp
 // takes kMergeRows rows side by side (a row is one load per lane and part) to
-// keep enough loads in flight (measured at 148 cut units of 256 rows: 16 us
-// with one row per warp). Grid (groups of 4 kMergeRows rows, cut units).
+// keep enough loads in flight (148 cut units of 256 rows took 16 us with one
+// row per warp). Many parts (few units, a long cache): the block's warps share
+// the parts of kMergeRows rows. Blocks go through (cut unit, group of rows)
+// with the grid's stride, as the number of cut units is known on the device
+// only.
 constexpr int kMergeRows = 4;
 template <int D>
 __global__ void __launch_bounds__(128) packed_merge_kernel(const PkArgs a) {
-  pdl_wait();
-  if (static_cast<int>(blockIdx.y) >= a.head->splits) return;
   constexpr int rows = PkCfg<D>::T * kBM;
+  constexpr int groups = rows / kMergeRows;
   constexpr int VW = D / 32;
-  const PlanSplit sp = a.split_list[blockIdx.y];
+  __shared__ float s_acc[4][kMergeRows][D], s_m[4][kMergeRows], s_den[4][kMergeRows];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rw0 = (blockIdx.x * 4 + warp) * kMergeRows;
-  const long long part0 = static_cast<long long>(sp.slot0) * rows + rw0;
-  // Rows of the tile, and of these the ones that hold a token: the others'
-  // partials were never written.
-  bool mine[kMergeRows];
-  int tok[kMergeRows], head[kMergeRows];
-  float acc[kMergeRows][VW], m[kMergeRows], den[kMergeRows];
-#pragma unroll
-  for (int i = 0; i < kMergeRows; ++i) {
-    const int t = (rw0 + i) / kBM, rt = (rw0 + i) % kBM;
-    tok[i] = sp.tok0 + t * a.TT + rt / a.r;
-    head[i] = sp.kvh * a.r + rt % a.r;
-    mine[i] = rt < a.TT * a.r && tok[i] < sp.n;
-    m[i] = -CUDART_INF_F;
-    den[i] = 0.f;
-#pragma unroll
-    for (int k = 0; k < VW; ++k) acc[i][k] = 0.f;
-  }
-#pragma unroll 2
-  for (int p = 0; p < sp.parts; ++p) {
-    float L[kMergeRows], x[kMergeRows][VW];
+  pdl_wait();
+  // First the units of few parts, four groups per block; then the others, if
+  // there are any (the plan counts them).
+  const int splits = a.head->splits;
+  const int few_work = splits * (groups / 4), work = few_work + (a.head->taken > 0 ? splits * groups : 0);
+#pragma unroll 1
+  for (int g = blockIdx.x; g < work; g += gridDim.x) {
+    const bool many = g >= few_work;
+    const int in_pass = many ? g - few_work : g, per_unit = many ? groups : groups / 4;
+    const PlanSplit sp = a.split_list[in_pass / per_unit];
+    if ((sp.parts > kMergeManyParts) != many) continue;
+    const int group = in_pass % per_unit;
+    const int rw0 = (many ? group : group * 4 + warp) * kMergeRows;
+    const long long part0 = static_cast<long long>(sp.slot0) * rows + rw0;
+    // Rows of the tile, and of these the ones that hold a token: the others'
+    // partials were never written.
+    bool mine[kMergeRows];
+    int tok[kMergeRows], head[kMergeRows];
+    float acc[kMergeRows][VW], m[kMergeRows], den[kMergeRows];
 #pragma unroll
     for (int i = 0; i < kMergeRows; ++i) {
-      const long long at = part0 + static_cast<long long>(p) * rows + i;
-      L[i] = mine[i] ? a.part_l[at] : -CUDART_INF_F;
-      if (mine[i])
-        load_vec(a.part_o + at * D + lane * VW, x[i]);
-      else
+      const int t = (rw0 + i) / kBM, rt = (rw0 + i) % kBM;
+      tok[i] = sp.tok0 + t * a.TT + rt / a.r;
+      head[i] = sp.kvh * a.r + rt % a.r;
+      mine[i] = rt < a.TT * a.r && tok[i] < sp.n;
+      m[i] = -CUDART_INF_F;
+      den[i] = 0.f;
 #pragma unroll
-        for (int k = 0; k < VW; ++k) x[i][k] = 0.f;
+      for (int k = 0; k < VW; ++k) acc[i][k] = 0.f;
     }
-#pragma unroll
-    for (int i = 0; i < kMergeRows; ++i) {
-      const float top = fmaxf(m[i], L[i]);
+    // One more part (or sum of parts) with maximum or logsumexp L, weight sum d
+    // and weighted row x into row i.
+    auto add = [&](int i, float L, float d, const float (&x)[VW]) {
+      const float top = fmaxf(m[i], L);
       const float ref = top == -CUDART_INF_F ? 0.f : top;  // no key so far: every weight 0
-      const float old = expf(m[i] - ref), wt = expf(L[i] - ref);
+      const float old = expf(m[i] - ref), wt = expf(L - ref);
       m[i] = top;
-      den[i] = den[i] * old + wt;
+      den[i] = den[i] * old + wt * d;
 #pragma unroll
-      for (int k = 0; k < VW; ++k) acc[i][k] = acc[i][k] * old + (wt == 0.f ? 0.f : wt * x[i][k]);
+      for (int k = 0; k < VW; ++k) acc[i][k] = acc[i][k] * old + (wt == 0.f ? 0.f : wt * x[k]);
+    };
+#pragma unroll 2
+    for (int p = many ? warp : 0; p < sp.parts; p += many ? 4 : 1) {
+      float L[kMergeRows], x[kMergeRows][VW];
+#pragma unroll
+      for (int i = 0; i < kMergeRows; ++i) {
+        const long long at = part0 + static_cast<long long>(p) * rows + i;
+        L[i] = mine[i] ? a.part_l[at] : -CUDART_INF_F;
+        if (mine[i])
+          load_vec(a.part_o + at * D + lane * VW, x[i]);
+        else
+#pragma unroll
+          for (int k = 0; k < VW; ++k) x[i][k] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < kMergeRows; ++i) add(i, L[i], 1.f, x[i]);
     }
-  }
+    if (many) {
+      // The warps' sums, in warp order; warp 0 stores.
+      __syncthreads();  // the last group's have been read
 #pragma unroll
-  for (int i = 0; i < kMergeRows; ++i) {
-    if (!mine[i]) continue;
-    const float inv = den[i] == 0.f ? 0.f : 1.f / den[i];
-    const long long row = static_cast<long long>(sp.base) + tok[i];
-    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.o.p) + row * a.o.ts + head[i] * a.o.hs +
-                                                lane * VW);
+      for (int i = 0; i < kMergeRows; ++i) {
 #pragma unroll
-    for (int k = 0; k < VW / 2; ++k) dst[k] = pack_bf16x2(acc[i][2 * k] * inv, acc[i][2 * k + 1] * inv);
-    if (lane == 0)
-      a.lse[static_cast<long long>(head[i]) * a.total + row] = den[i] == 0.f ? -CUDART_INF_F : m[i] + logf(den[i]);
+        for (int k = 0; k < VW; ++k) s_acc[warp][i][lane * VW + k] = acc[i][k];
+        if (lane == 0) {
+          s_m[warp][i] = m[i];
+          s_den[warp][i] = den[i];
+        }
+      }
+      __syncthreads();
+      if (warp > 0) continue;
+#pragma unroll
+      for (int v = 1; v < 4; ++v)
+#pragma unroll
+        for (int i = 0; i < kMergeRows; ++i) {
+          float x[VW];
+#pragma unroll
+          for (int k = 0; k < VW; ++k) x[k] = s_acc[v][i][lane * VW + k];
+          add(i, s_m[v][i], s_den[v][i], x);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kMergeRows; ++i) {
+      if (!mine[i]) continue;
+      const float inv = den[i] == 0.f ? 0.f : 1.f / den[i];
+      const long long row = static_cast<long long>(sp.base) + tok[i];
+      uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.o.p) + row * a.o.ts + head[i] * a.o.hs +
+                                                  lane * VW);
+      uint32_t* rst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.resid.p) + row * a.resid.ts +
+                                                  head[i] * a.resid.hs + lane * VW);
+#pragma unroll
+      for (int k = 0; k < VW / 2; ++k) {
+        const float x0 = acc[i][2 * k] * inv, x1 = acc[i][2 * k + 1] * inv;
+        const uint32_t o = pack_bf16x2(x0, x1);
+        dst[k] = o;
+        if (a.resid.p) {
+          const __nv_bfloat162 hi = *reinterpret_cast<const __nv_bfloat162*>(&o);
+          rst[k] = pack_bf16x2(x0 - __low2float(hi), x1 - __high2float(hi));
+        }
+      }
+      if (lane == 0)
+        a.lse[static_cast<long long>(head[i]) * a.total + row] = den[i] == 0.f ? -CUDART_INF_F : m[i] + logf(den[i]);
+    }
   }
 }
 
@@ -817,17 +871,22 @@ Layout make_layout(const SeqShape& s, const CacheShape* c, int ctas) {
   x.TT = kBM / s.r();
   x.unit = tiles * x.TT;
   x.max_items = plan_max_units(s.S, s.T, x.unit);
-  // Runs only over a cache, and where there can be so few units (plan_runs()
-  // decides on the device); the cost sums stay in 32 bits.
+  // Runs where there can be so few units (the plan decides), of prompts fewer
+  // than CTAs: their keys are no more than their queries, and the merge's launch
+  // costs a microsecond. The sums of their costs stay in 32 bits.
   const long long least = (static_cast<long long>(s.T) + x.unit - 1) / x.unit;
-  x.runs = c && s.S <= kPlanSeqs && least * s.Hkv < static_cast<long long>(kRunUnits) &&
-           (static_cast<long long>(c->max_pages) * c->page / kBN + 4) * 4 * kRunUnits < (1LL << 31);
+  const long long keys = c ? static_cast<long long>(c->max_pages) * c->page : s.T;
+  const long long key_tiles = (keys + kBN - 1) / kBN + 1;
+  x.runs = s.S <= kPlanSeqs && least * s.Hkv < static_cast<long long>(c ? kRunUnits : ctas) &&
+           (key_tiles + 4) * kCostTile * kRunUnits < (1LL << 31);
   const int grid = tiles == 2 ? ctas : 2 * ctas;
   x.max_parts = 0;
   if (x.runs) {
-    // Each run boundary adds an item and cuts at most one unit.
+    // Each run boundary adds an item and cuts at most one unit; the parts of a
+    // unit are kRunLeast key tiles or more.
+    const long long most = x.max_items * s.Hkv * (key_tiles / kRunLeast);
+    x.max_parts = most < 2 * grid ? static_cast<int>(most) : 2 * grid;
     x.max_items += kRunUnits + grid;
-    x.max_parts = 2 * grid;
   }
   x.plan = plan_layout(x.max_items, x.runs ? grid : 0, x.runs ? grid : 0);
   x.off_o = x.plan.bytes;
@@ -836,13 +895,13 @@ Layout make_layout(const SeqShape& s, const CacheShape* c, int ctas) {
   return x;
 }
 
-template <int D, bool PAGED>
+template <int D, bool PAGED, bool RUNS>
 cudaError_t launch_t(const SeqShape& s, const CacheShape* c, const Layout& x, const CUtensorMap& tq,
                      const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& to, const CUtensorMap& tr,
                      const Rows& o, const Rows& resid, float* lse, void* workspace, int sms, const LaunchCtl& ctl,
                      cudaStream_t stream) {
   using C = PkCfg<D>;
-  auto kern = packed_fwd_kernel<D, PAGED>;
+  auto kern = packed_fwd_kernel<D, PAGED, RUNS>;
   static SmemOnce once;
   cudaError_t e = once.set(reinterpret_cast<const void*>(kern), C::kSmemBytes);
   if (e != cudaSuccess) return e;
@@ -908,7 +967,7 @@ cudaError_t launch_t(const SeqShape& s, const CacheShape* c, const Layout& x, co
   e = launch_dependent(kern, dim3(static_cast<unsigned>(grid)), C::kThreads, C::kSmemBytes, stream, tq, tk, tv, to, tr,
                        a);
   if (e != cudaSuccess || !x.runs) return e;
-  return launch_dependent(packed_merge_kernel<D>, dim3(C::T * kBM / (4 * kMergeRows), C::kMinBlocks * sms), 128, 0, stream, a);
+  return launch_dependent(packed_merge_kernel<D>, dim3(8 * sms), 128, 0, stream, a);
 }
 
 }  // namespace
@@ -934,8 +993,12 @@ cudaError_t launch_packed_fwd(const SeqShape& s, const CacheShape* c, const Rows
   }
   if (!ok) return cudaErrorInvalidValue;
 #define FA_ARGS s, c, x, tq, tk, tv, to, tr, o, resid, lse, workspace, sms, ctl, stream
-  if (s.d == 64) return c ? launch_t<64, true>(FA_ARGS) : launch_t<64, false>(FA_ARGS);
-  return c ? launch_t<128, true>(FA_ARGS) : launch_t<128, false>(FA_ARGS);
+  if (s.d == 64) {
+    if (c) return launch_t<64, true, true>(FA_ARGS);
+    return x.runs ? launch_t<64, false, true>(FA_ARGS) : launch_t<64, false, false>(FA_ARGS);
+  }
+  if (c) return launch_t<128, true, true>(FA_ARGS);
+  return x.runs ? launch_t<128, false, true>(FA_ARGS) : launch_t<128, false, false>(FA_ARGS);
 #undef FA_ARGS
 }
 

@@ -17,8 +17,10 @@ namespace fa {
 struct PlanHeader {
   int items;   // items listed
   int splits;  // units cut along the keys (paged chunks)
-  int taken;   // forward: items taken by the CTAs beyond their first
-  int runs;    // nonzero: CTA c takes items [run_first[c], run_first[c + 1])
+  int taken;   // forward: items taken by the CTAs beyond their first; of runs: units of more
+               // than kMergeManyParts parts
+  int runs;    // forward: CTA c takes items [run_first[c], run_first[c + 1]);
+               // backward: the items are parts of units
 };
 
 // A unit and KV head cut along the keys: parts slot0, slot0 + 1, ... of the partial
@@ -38,6 +40,8 @@ struct PlanArgs {
   int heads;       // CTAs per item (KV heads)
   int run_ctas;    // > 0: the work may be cut into this many runs
   int half;        // units of at most this many tokens take less time (0: none)
+  int r;           // backward: query heads of a KV head, gone through one after another
+  int part_ctas;   // backward: > 0: units may be cut into parts for this many CTAs
   int sorted;      // 0: every CTA is resident at once, any order does
   PlanHeader* head;
   PlanItem* items;
@@ -48,6 +52,11 @@ struct PlanArgs {
 
 constexpr int kPlanSeqs = 1024;    // sequences held in shared memory at a time
 constexpr int kPlanBuckets = 1024;
+// Units of more parts than this are merged by more warps.
+constexpr int kMergeManyParts = 8;
+// Backward: no part of a unit is shorter than this many steps (a CTA's start
+// and end take as long as five).
+constexpr int kPartSteps = 8;
 // Runs are made of fewer units times KV heads than this; more units are
 // balanced well enough by taking them longest first (4 per CTA).
 constexpr int kRunUnits = 4 * 148;
@@ -55,7 +64,11 @@ constexpr int kRunUnits = 4 * 148;
 // tile, and of starting and ending an item, in quarters of a tile (measured
 // at d = 128: 1.7 us a tile, 4 us an item, part of it beside its neighbours).
 constexpr int kCostTile = 4, kCostHalf = 3, kCostItem = 6;
-// No run end cuts off less than this many key tiles of a unit.
+// No run is shorter than this (about six key tiles), so that few units are not
+// cut into more parts than their merge is worth; and no run end cuts off less
+// than kRunLeast key tiles of a unit.
+constexpr int kCostMerge = 20;  // the parts' stores and the merge kernel, about 8 us
+constexpr int kRunCost = kCostItem + 6 * kCostTile;
 constexpr int kRunLeast = 3;
 
 struct PlanShared {
@@ -64,7 +77,7 @@ struct PlanShared {
   int hist[kPlanBuckets];
   int warp_sum[32];
   int upos[kRunUnits + 1];  // units' costs, summed
-  int n_splits, n_slots;
+  int most, n_splits, n_slots, n_many;
 };
 
 // Inclusive sum of `x` over the block of NT threads.
@@ -147,7 +160,7 @@ __device__ void plan_block(const PlanArgs& a, PlanShared& sh) {
     const int n = sh.n[lo], tok0 = (u - sh.pre[lo]) * a.unit;
     const int w = a.backward ? (n + 63) / 64 - (a.causal ? tok0 / 64 : 0)
                              : plan_fwd_tiles(n, sh.len[lo], tok0, a.unit, a.causal);
-    it = PlanItem{sh.start[lo], n, sh.len[lo] - n, tok0, 0, w, -1, b0 + lo, -1};
+    it = PlanItem{sh.start[lo], n, sh.len[lo] - n, tok0, 0, a.backward ? w * a.r : w, -1, b0 + lo, -1};
     return w;
   };
   // f(u, item, work) for every unit.
@@ -168,7 +181,7 @@ __device__ void plan_block(const PlanArgs& a, PlanShared& sh) {
     }
   };
   for (int i = threadIdx.x; i < kPlanBuckets; i += NT) sh.hist[i] = 0;
-  if (threadIdx.x == 0) sh.n_splits = sh.n_slots = 0;
+  if (threadIdx.x == 0) sh.most = sh.n_splits = sh.n_slots = sh.n_many = 0;
   int U = 0;
   if (one_chunk) {
     U = held_units = load(0);
@@ -190,7 +203,7 @@ __device__ void plan_block(const PlanArgs& a, PlanShared& sh) {
   }
   if (a.run_ctas > 0 && static_cast<long long>(U) * a.heads < kRunUnits) {
     // Cost of each unit, summed; a run is 1 / run_ctas of all units' and heads'.
-    int total = 0;
+    int total = 0, most = 0;
 #pragma unroll 1
     for (int u0 = 0; u0 < U; u0 += NT) {
       const int u = u0 + threadIdx.x;
@@ -203,71 +216,106 @@ __device__ void plan_block(const PlanArgs& a, PlanShared& sh) {
       const int x = plan_scan<NT>(cost, sh.warp_sum, sum);
       if (u < U) sh.upos[u + 1] = total + x;
       total += sum;
+      most = max(most, cost);
     }
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) atomicMax(&sh.most, most);
     if (threadIdx.x == 0) sh.upos[0] = 0;
     __syncthreads();
-    const int len = max(1, (total * a.heads + a.run_ctas - 1) / a.run_ctas);
-    // First pass: the runs' sizes; second: the items, from their starts on.
+    const int mean = (total * a.heads + a.run_ctas - 1) / a.run_ctas;
+    const int len = max(kRunCost, mean);
+    // Taken one by one, longest first, the units end about when their mean per
+    // CTA plus most of the longest has passed; runs end together, and their
+    // merge follows.
+    if (mean + sh.most * 4 / 5 > len + kCostMerge) {
+      // First pass: the runs' sizes; second: the items, from their starts on.
 #pragma unroll 1
-    for (int pass = 0; pass < 2; ++pass) {
+      for (int pass = 0; pass < 2; ++pass) {
 #pragma unroll 1
-      for (int q = threadIdx.x; q < U * a.heads; q += NT) {
-        const int u = q / a.heads;
-        PlanItem it;
-        const int w = unit_of(0, u, it);
-        it.kvh = q - u * a.heads;
-        const int cost = sh.upos[u + 1] - sh.upos[u];
-        const int at = sh.upos[u] * a.heads + it.kvh * cost;
-        const int per = it.n - it.tok0 <= a.half ? kCostHalf : kCostTile;
-        // Key tile at which run r ends within this unit.
-        auto end_tile = [&](int r) {
-          const int x = (r + 1) * len - at;
-          if (x >= cost) return w;
-          const int j = (x - kCostItem) / per;
-          return j < kRunLeast ? 0 : (j > w - kRunLeast ? w : j);
-        };
-        int parts = 0, done = 0;
+        for (int q = threadIdx.x; q < U * a.heads; q += NT) {
+          const int u = q / a.heads;
+          PlanItem it;
+          const int w = unit_of(0, u, it);
+          it.kvh = q - u * a.heads;
+          const int cost = sh.upos[u + 1] - sh.upos[u];
+          const int at = sh.upos[u] * a.heads + it.kvh * cost;
+          const int per = it.n - it.tok0 <= a.half ? kCostHalf : kCostTile;
+          // Key tile at which run r ends within this unit.
+          auto end_tile = [&](int r) {
+            const int x = (r + 1) * len - at;
+            if (x >= cost) return w;
+            const int j = (x - kCostItem) / per;
+            return j < kRunLeast ? 0 : (j > w - kRunLeast ? w : j);
+          };
+          int parts = 0, done = 0;
 #pragma unroll 1
-        for (int r = at / len; done < w; ++r) {
-          const int e = end_tile(r);
-          if (e > done) ++parts;
-          done = max(done, e);
+          for (int r = at / len; done < w; ++r) {
+            const int e = end_tile(r);
+            if (e > done) ++parts;
+            done = max(done, e);
+          }
+          if (pass == 1 && parts > 1) {
+            it.slot = atomicAdd(&sh.n_slots, parts);
+            if (parts > kMergeManyParts) atomicAdd(&sh.n_many, 1);
+            a.split_list[atomicAdd(&sh.n_splits, 1)] = PlanSplit{it.base, it.n, it.tok0, it.kvh, it.slot, parts};
+          }
+          done = 0;
+#pragma unroll 1
+          for (int r = at / len; done < w; ++r) {
+            const int e = end_tile(r);
+            if (e <= done) continue;
+            const int place = atomicAdd(&sh.hist[r], 1);
+            it.j0 = done;
+            it.j1 = done = e;
+            if (pass == 1) a.items[place] = it;
+            if (parts > 1) ++it.slot;
+          }
         }
-        if (pass == 1 && parts > 1) {
-          it.slot = atomicAdd(&sh.n_slots, parts);
-          a.split_list[atomicAdd(&sh.n_splits, 1)] = PlanSplit{it.base, it.n, it.tok0, it.kvh, it.slot, parts};
-        }
-        done = 0;
+        __syncthreads();
+        if (pass == 1) break;
+        int run = 0;
 #pragma unroll 1
-        for (int r = at / len; done < w; ++r) {
-          const int e = end_tile(r);
-          if (e <= done) continue;
-          const int place = atomicAdd(&sh.hist[r], 1);
-          it.j0 = done;
-          it.j1 = done = e;
-          if (pass == 1) a.items[place] = it;
-          if (parts > 1) ++it.slot;
+        for (int i0 = 0; i0 < a.run_ctas; i0 += NT) {
+          const int i = i0 + threadIdx.x;
+          const int h = i < a.run_ctas ? sh.hist[i] : 0;
+          int sum;
+          const int x = run + plan_scan<NT>(h, sh.warp_sum, sum);
+          if (i < a.run_ctas) {
+            sh.hist[i] = x - h;
+            a.run_first[i + 1] = x;
+          }
+          run += sum;
         }
+        if (threadIdx.x == 0) a.run_first[0] = 0;
+        __syncthreads();
       }
-      __syncthreads();
-      if (pass == 1) break;
-      int run = 0;
-#pragma unroll 1
-      for (int i0 = 0; i0 < a.run_ctas; i0 += NT) {
-        const int i = i0 + threadIdx.x;
-        const int h = i < a.run_ctas ? sh.hist[i] : 0;
-        int sum;
-        const int x = run + plan_scan<NT>(h, sh.warp_sum, sum);
-        if (i < a.run_ctas) {
-          sh.hist[i] = x - h;
-          a.run_first[i + 1] = x;
-        }
-        run += sum;
-      }
-      if (threadIdx.x == 0) a.run_first[0] = 0;
-      __syncthreads();
+      if (threadIdx.x == 0) *a.head = PlanHeader{U * a.heads, sh.n_splits, sh.n_many, 1};
+      return;
     }
-    if (threadIdx.x == 0) *a.head = PlanHeader{U * a.heads, sh.n_splits, 0, 1};
+  }
+  const int free_ctas = a.part_ctas / a.heads - U;  // of each KV head's share, beyond one per unit
+  if (a.part_ctas > 0 && U > 0 && free_ctas > 0) {
+    // Backward with fewer units than CTAs: each unit's (head, query tile)
+    // steps are cut into parts of at most len steps, such that one wave holds
+    // them all; the parts add up dK and dV in fp32.
+    int steps = 0;
+    each([&](int, const PlanItem& it, int) { steps += it.j1; });
+    steps = __reduce_add_sync(0xffffffffu, steps);
+    if (lane == 0) atomicAdd(&sh.most, steps);
+    __syncthreads();
+    const int len = max(kPartSteps, (sh.most + free_ctas - 1) / free_ctas);
+    each([&](int, PlanItem it, int) {
+      const int all = it.j1, parts = (all + len - 1) / len;
+      int at = atomicAdd(&sh.n_slots, parts);
+#pragma unroll 1
+      for (int k = 0; k < parts; ++k, ++at) {
+        it.j1 = it.j0 + all / parts + (k < all % parts ? 1 : 0);
+        a.items[at] = it;
+        it.j0 = it.j1;
+      }
+    });
+    __syncthreads();
+    if (threadIdx.x == 0) *a.head = PlanHeader{sh.n_slots, 0, 0, 1};
     return;
   }
   if (!a.sorted) {

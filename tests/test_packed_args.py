@@ -100,10 +100,12 @@ def test_workspaces():
     assert L.fa_packed_fwd_workspace_bytes(2, 64, 4, 3, 64) == 0 and L.fa_packed_fwd_workspace_bytes(2, 64, 4, 2, 96) == 0
     assert L.fa_packed_bwd_workspace_bytes(-1, 64, 4, 2, 64) == 0
     assert L.fa_paged_fwd_workspace_bytes(2, 64, 8, 4, 2, 64, 12, 8) == 0
-    # The backward holds an fp32 D and dQ per query row; the forward a list of its units.
+    # The backward holds an fp32 D and dQ per query row; the forward a list of its units, and partial results only
+    # where the units can be few.
     n = L.fa_packed_bwd_workspace_bytes(3, 1000, 4, 2, 128)
-    assert 4 * 4 * 1000 * 129 <= n < 4 * 4 * 1000 * 129 + (1 << 16)
-    assert 0 < L.fa_packed_fwd_workspace_bytes(3, 1000, 4, 2, 128) < 1 << 16
+    assert 4 * 4 * 1000 * 129 <= n < 4 * 4 * 1000 * 129 + (1 << 22)
+    assert 0 < L.fa_packed_fwd_workspace_bytes(3, 1000, 4, 2, 128) < 1 << 24
+    assert 0 < L.fa_packed_fwd_workspace_bytes(8, 1 << 17, 32, 8, 128) < 1 << 18
     # Paged: partial results; more rows per sequence need more.
     one = L.fa_paged_fwd_workspace_bytes(32, 32, 1, 32, 8, 128, 16, 512)
     four = L.fa_paged_fwd_workspace_bytes(32, 128, 4, 32, 8, 128, 16, 512)
