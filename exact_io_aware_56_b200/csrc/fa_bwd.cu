@@ -1010,10 +1010,9 @@ struct PackedBwdLayout {
 PackedBwdLayout packed_bwd_layout(const SeqShape& s) {
   PackedBwdLayout x;
   x.max_items = plan_max_units(s.S, s.T, kKT);
-  // Where there can be fewer units than CTAs; a KV head's share of the CTAs
-  // bounds its parts.
-  x.parts = (static_cast<long long>(s.T) + kKT - 1) / kKT * s.Hkv < kPartCtas;
-  if (x.parts) x.max_items += kPartCtas;
+  // Where there can be so few units (the plan decides).
+  x.parts = (static_cast<long long>(s.T) + kKT - 1) / kKT * s.Hkv < kPartUnits;
+  if (x.parts && x.max_items * s.Hkv < kPartWaves * kPartCtas) x.max_items = (kPartWaves * kPartCtas + s.Hkv - 1) / s.Hkv;
   x.plan = plan_layout(x.max_items, 0, 0);
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   x.off_d = up(x.plan.bytes);

@@ -880,6 +880,10 @@ Layout make_layout(const SeqShape& s, const CacheShape* c, int ctas) {
   x.runs = s.S <= kPlanSeqs && least * s.Hkv < static_cast<long long>(c ? kRunUnits : ctas) &&
            (key_tiles + 4) * kCostTile * kRunUnits < (1LL << 31);
   const int grid = tiles == 2 ? ctas : 2 * ctas;
+  // (The plan's own condition, for the longest units that there can be.)
+  const long long most_cost = kCostItem + kCostTile * key_tiles;
+  const long long mean_cost = x.max_items * s.Hkv * most_cost / grid;
+  if (!plan_wants_runs(mean_cost, most_cost)) x.runs = false;
   x.max_parts = 0;
   if (x.runs) {
     // Each run boundary adds an item and cuts at most one unit; the parts of a

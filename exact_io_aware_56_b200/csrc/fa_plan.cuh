@@ -54,9 +54,13 @@ constexpr int kPlanSeqs = 1024;    // sequences held in shared memory at a time
 constexpr int kPlanBuckets = 1024;
 // Units of more parts than this are merged by more warps.
 constexpr int kMergeManyParts = 8;
-// Backward: no part of a unit is shorter than this many steps (a CTA's start
-// and end take as long as five).
-constexpr int kPartSteps = 8;
+// Backward: units times KV heads below which units may be cut into parts, for
+// how many waves of CTAs at most, the least steps of a part, and what a CTA's
+// start and end take, in steps.
+constexpr int kPartUnits = 256;
+constexpr int kPartWaves = 3;
+constexpr int kPartLeast = 6;
+constexpr int kPartSteps = 5;
 // Runs are made of fewer units times KV heads than this; more units are
 // balanced well enough by taking them longest first (4 per CTA).
 constexpr int kRunUnits = 4 * 148;
@@ -67,9 +71,16 @@ constexpr int kCostTile = 4, kCostHalf = 3, kCostItem = 6;
 // No run is shorter than this (about six key tiles), so that few units are not
 // cut into more parts than their merge is worth; and no run end cuts off less
 // than kRunLeast key tiles of a unit.
-constexpr int kCostMerge = 20;  // the parts' stores and the merge kernel, about 8 us
+constexpr int kCostMerge = 36;  // the parts' stores and the merge kernel, about 14 us
 constexpr int kRunCost = kCostItem + 6 * kCostTile;
 constexpr int kRunLeast = 3;
+
+// Taken one by one, longest first, the units end about when their mean cost per
+// CTA plus most of the longest's has passed; runs end together, no earlier
+// than the least run, and their merge follows.
+__host__ __device__ inline bool plan_wants_runs(long long mean, long long most) {
+  return mean + most * 4 / 5 > (mean > kRunCost ? mean : kRunCost) + kCostMerge;
+}
 
 struct PlanShared {
   int pre[kPlanSeqs + 1];  // units of the held sequences, summed
@@ -224,10 +235,7 @@ __device__ void plan_block(const PlanArgs& a, PlanShared& sh) {
     __syncthreads();
     const int mean = (total * a.heads + a.run_ctas - 1) / a.run_ctas;
     const int len = max(kRunCost, mean);
-    // Taken one by one, longest first, the units end about when their mean per
-    // CTA plus most of the longest has passed; runs end together, and their
-    // merge follows.
-    if (mean + sh.most * 4 / 5 > len + kCostMerge) {
+    if (plan_wants_runs(mean, sh.most)) {
       // First pass: the runs' sizes; second: the items, from their starts on.
 #pragma unroll 1
       for (int pass = 0; pass < 2; ++pass) {
@@ -293,50 +301,68 @@ __device__ void plan_block(const PlanArgs& a, PlanShared& sh) {
       return;
     }
   }
-  const int free_ctas = a.part_ctas / a.heads - U;  // of each KV head's share, beyond one per unit
-  if (a.part_ctas > 0 && U > 0 && free_ctas > 0) {
-    // Backward with fewer units than CTAs: each unit's (head, query tile)
-    // steps are cut into parts of at most len steps, such that one wave holds
-    // them all; the parts add up dK and dV in fp32.
-    int steps = 0;
-    each([&](int, const PlanItem& it, int) { steps += it.j1; });
-    steps = __reduce_add_sync(0xffffffffu, steps);
-    if (lane == 0) atomicAdd(&sh.most, steps);
-    __syncthreads();
-    const int len = max(kPartSteps, (sh.most + free_ctas - 1) / free_ctas);
-    each([&](int, PlanItem it, int) {
-      const int all = it.j1, parts = (all + len - 1) / len;
-      int at = atomicAdd(&sh.n_slots, parts);
-#pragma unroll 1
-      for (int k = 0; k < parts; ++k, ++at) {
-        it.j1 = it.j0 + all / parts + (k < all % parts ? 1 : 0);
-        a.items[at] = it;
-        it.j0 = it.j1;
-      }
+  // Backward with few units: each unit's (head, query tile) steps may be cut
+  // into parts of at most len steps, which add up dK and dV in fp32. Parts for
+  // one, two or three waves of CTAs against whole units, by what each takes at
+  // most: waves times the longest part, or (whole units) the mean per CTA plus
+  // the longest.
+  int len = 0x7fffffff;
+  bool parts_used = false;
+  if (a.part_ctas > 0 && static_cast<long long>(U) * a.heads < kPartUnits) {
+    int most = 0, steps = 0;
+    each([&](int, const PlanItem& it, int) {
+      steps += it.j1;
+      most = max(most, it.j1);
     });
+    most = __reduce_max_sync(0xffffffffu, most);
+    steps = __reduce_add_sync(0xffffffffu, steps);
+    if (lane == 0) {
+      atomicMax(&sh.most, most);
+      atomicAdd(&sh.n_slots, steps);
+    }
     __syncthreads();
-    if (threadIdx.x == 0) *a.head = PlanHeader{sh.n_slots, 0, 0, 1};
-    return;
+    const int waves = (U * a.heads + a.part_ctas - 1) / a.part_ctas;
+    const int mean = (sh.n_slots + kPartSteps * U) * a.heads / a.part_ctas;
+    int best = min(waves * (sh.most + kPartSteps), mean + sh.most + kPartSteps) * 7 / 8;  // a cut has to gain that much
+#pragma unroll 1
+    for (int k = 1; k <= kPartWaves; ++k) {
+      const int room = k * a.part_ctas / a.heads - U;  // parts of a KV head beyond one per unit
+      if (room <= 0) continue;
+      const int l = max(kPartLeast, (sh.n_slots + room - 1) / room);
+      const int cost = k * (l + kPartSteps);
+      if (cost < best) {
+        best = cost;
+        len = l;
+        parts_used = true;
+      }
+    }
   }
-  if (!a.sorted) {
+  if (!parts_used && (!a.sorted || static_cast<long long>(U) * a.heads <= a.part_ctas)) {
     each([&](int u, const PlanItem& it, int) { a.items[u] = it; });
     if (threadIdx.x == 0) *a.head = PlanHeader{U, 0, 0, 0};
     return;
   }
   // Longest first: bucket 0 holds the longest.
-  const long long most = a.backward ? a.T / 64 + 1 : a.max_len / 128 + 1;
+  const long long most = a.backward ? (a.T / 64 + 1LL) * a.r : a.max_len / 128 + 1;
   int shift = 0;
   while ((most >> shift) >= kPlanBuckets) ++shift;
   // First pass: the buckets' sizes; second: the items, from their starts on.
+  int run = 0;
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
-    each([&](int, const PlanItem& it, int w) {
-      const int at = atomicAdd(&sh.hist[kPlanBuckets - 1 - (w >> shift)], 1);
-      if (pass == 1) a.items[at] = it;
+    each([&](int, PlanItem it, int) {
+      const int all = it.j1, parts = parts_used ? (all + len - 1) / len : 1;
+#pragma unroll 1
+      for (int k = 0; k < parts; ++k) {
+        const int n = parts == 1 ? all : all / parts + (k < all % parts ? 1 : 0);
+        const int at = atomicAdd(&sh.hist[kPlanBuckets - 1 - (n >> shift)], 1);
+        it.j1 = it.j0 + n;
+        if (pass == 1) a.items[at] = it;
+        it.j0 = it.j1;
+      }
     });
     __syncthreads();
     if (pass == 1) break;
-    int run = 0;
 #pragma unroll 1
     for (int i0 = 0; i0 < kPlanBuckets; i0 += NT) {
       const int i = i0 + threadIdx.x;
@@ -348,7 +374,7 @@ __device__ void plan_block(const PlanArgs& a, PlanShared& sh) {
     }
     __syncthreads();
   }
-  if (threadIdx.x == 0) *a.head = PlanHeader{U, 0, 0, 0};
+  if (threadIdx.x == 0) *a.head = PlanHeader{run, 0, 0, parts_used ? 1 : 0};
 }
 
 __device__ __forceinline__ PlanItem load_item(const PlanItem* p) {
