@@ -874,12 +874,12 @@ Layout make_layout(const SeqShape& s, const CacheShape* c, int ctas) {
   // Runs where there can be so few units (the plan decides), of prompts fewer
   // than CTAs: their keys are no more than their queries, and the merge's launch
   // costs a microsecond. The sums of their costs stay in 32 bits.
+  const int grid = tiles == 2 ? ctas : 2 * ctas;
   const long long least = (static_cast<long long>(s.T) + x.unit - 1) / x.unit;
   const long long keys = c ? static_cast<long long>(c->max_pages) * c->page : s.T;
   const long long key_tiles = (keys + kBN - 1) / kBN + 1;
-  x.runs = s.S <= kPlanSeqs && least * s.Hkv < static_cast<long long>(c ? kRunUnits : ctas) &&
+  x.runs = s.S <= kPlanSeqs && least * s.Hkv < static_cast<long long>(c ? kRunUnits : grid) &&
            (key_tiles + 4) * kCostTile * kRunUnits < (1LL << 31);
-  const int grid = tiles == 2 ? ctas : 2 * ctas;
   // (The plan's own condition, for the longest units that there can be.)
   const long long most_cost = kCostItem + kCostTile * key_tiles;
   const long long mean_cost = x.max_items * s.Hkv * most_cost / grid;

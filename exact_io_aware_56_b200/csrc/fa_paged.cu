@@ -101,8 +101,17 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= 384, "barrier block exceeds its shared-memory reservation");
 
-// No more runs than tiles, so that none is empty (the merge counts on it).
-__device__ __forceinline__ int runs_of(long long W, int ctas) { return W < ctas ? (W < 1 ? 1 : static_cast<int>(W)) : ctas; }
+// Runs: one per CTA, but none empty (the merge counts on it), and of few units
+// over long caches none so short that merging a unit's partials takes longer
+// than the tiles it saves: of T tiles a unit in runs of k the longest run takes
+// 0.9 k us and the merge 0.06 rho T / k us (measured), least at
+// k = sqrt(0.07 rho T). Five sequences of up to 7.5k
+// keys, one KV head: 27.4 -> 20.6 us.
+__device__ __forceinline__ int runs_of(long long W, int ctas, int rho, int units) {
+  const int k = max(1, static_cast<int>(sqrtf(0.07f * rho * static_cast<float>(W) / units)));
+  const long long runs = W / k;
+  return runs < ctas ? (runs < 1 ? 1 : static_cast<int>(runs)) : ctas;
+}
 // First tile of run c of G; in 32 bits where they hold it (W G < 2^31).
 __device__ __forceinline__ long long run_lo(int c, long long W, int G) {
   if (W <= (1 << 22)) return static_cast<unsigned>(c) * static_cast<unsigned>(W) / static_cast<unsigned>(G);
@@ -162,7 +171,7 @@ __device__ __forceinline__ long long warp_scan(long long x, int lane) {
 // 32nd of the sequences; the 32nd that holds the run's first tile is then
 // looked through 32 sequences at a time. W: all tiles; 0 (no work at all)
 // where a length or an offset is out of range.
-__device__ __forceinline__ Cursor first_tile(const Args& a, int lane, long long& W, bool& bad) {
+__device__ __forceinline__ Cursor first_tile(const Args& a, int rho, int lane, long long& W, bool& bad) {
   const int per = (a.S + 31) / 32;
   long long mine = 0;
   bad = false;
@@ -173,7 +182,7 @@ __device__ __forceinline__ Cursor first_tile(const Args& a, int lane, long long&
   bad = __any_sync(0xffffffffu, bad);
   const long long incl = warp_scan(mine, lane);
   W = bad ? 0 : __shfl_sync(0xffffffffu, incl, 31) * a.Hkv;
-  const int G = runs_of(W, gridDim.x);
+  const int G = runs_of(W, gridDim.x, rho, a.S * a.Hkv);
   Cursor c;
   c.t = c.t_lo = run_lo(min(static_cast<int>(blockIdx.x), G), W, G);
   c.t_hi = run_lo(min(static_cast<int>(blockIdx.x) + 1, G), W, G);
@@ -254,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   long long W;
   bool bad;
-  const Cursor start = first_tile(a, lane, W, bad);
+  const Cursor start = first_tile(a, RHO, lane, W, bad);
   const long long t_lo = start.t_lo;
   auto all = [](bool b) { return __all_sync(0xffffffffu, b); };
 
@@ -631,7 +640,7 @@ __global__ void __launch_bounds__(128)
   const int Tb = static_cast<int>(a.tile_pre[b + 1] - pre);
   const long long W = a.tile_pre[a.S] * a.Hkv;
   if (Tb == 0 || rr >= n * a.r) return;
-  const int G = runs_of(W, ctas);
+  const int G = runs_of(W, ctas, rho, a.S * a.Hkv);
   const long long first = pre * a.Hkv + static_cast<long long>(kvh) * Tb;
   const int c0 = run_of(first, W, G);
   const int n_parts = (run_of(first + Tb - 1, W, G) - c0 + 1) * rho;
