@@ -110,6 +110,9 @@ struct PkArgs {
   float* part_o;  // [slot][T * 128][D]
   float* part_l;
   int total, Hkv, r, TT, causal;
+  // Packed, few units: no list; every CTA finds its units in cu itself.
+  int direct, S, unit;
+  const int* cu;
   int sectors;  // o (and its residual) can be stored 32 bytes at a time
   float scale_log2, rescale_tau;
   LaunchCtl ctl;
@@ -136,6 +139,51 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PlanArg
   __shared__ PlanShared sh;
   pdl_launch_dependents();
   plan_block<kPlanThreads>(a, sh);
+}
+
+// Units of all sequences, by the whole warp; 0, and reported, where an offset
+// is out of range.
+__device__ __forceinline__ int direct_units(const PkArgs& a, int lane) {
+  int n = 0;
+  bool bad = false;
+  for (int b = lane; b < a.S; b += 32) {
+    const SeqRange s = seq_range(a.cu, nullptr, b, a.total, a.total, a.total);
+    bad |= s.bad;
+    n += (s.n + a.unit - 1) / a.unit;
+  }
+  if (__any_sync(0xffffffffu, bad)) {
+    if (lane == 0 && blockIdx.x == 0) atomicOr(a.ctl.err, kErrData);
+    return 0;
+  }
+  return __reduce_add_sync(0xffffffffu, n);
+}
+
+// Unit u of them, by the whole warp: 32 sequences a step.
+__device__ __forceinline__ PlanItem direct_item(const PkArgs& a, int u, int lane) {
+  PlanItem it{};
+  int before = 0;
+  for (int b0 = 0; b0 < a.S; b0 += 32) {
+    SeqRange s{};
+    if (b0 + lane < a.S) s = seq_range(a.cu, nullptr, b0 + lane, a.total, a.total, a.total);
+    const int mine = (s.n + a.unit - 1) / a.unit;
+    int end = before + mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, end - before, o);
+      if (lane >= o) end += y;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, end > u);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      const int n = __shfl_sync(0xffffffffu, s.n, l);
+      const int tok0 = (u - __shfl_sync(0xffffffffu, end - mine, l)) * a.unit;
+      it = PlanItem{__shfl_sync(0xffffffffu, s.start, l), n, 0, tok0, 0,
+                    plan_fwd_tiles(n, n, tok0, a.unit, a.causal), -1, b0 + l, -1};
+      break;
+    }
+    before = __shfl_sync(0xffffffffu, end, 31);
+  }
+  return it;
 }
 
 // An item as a CTA works on it: tile t holds tokens [tok_t[t], ...) and takes
@@ -283,15 +331,29 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, PkCfg<D>::kMinBlocks)
       // Items of the list times the KV heads, taken one by one; or, where the
       // plan cut the work into runs, this CTA's own items.
       const bool runs = RUNS && a.head->runs != 0;
+      const bool direct = !PAGED && a.direct;
+      int units = 0;
+      if (direct) {
+        units = direct_units(a, lane);
+      } else {
+        units = a.head->items;
+      }
       int idx = runs ? a.run_first[blockIdx.x] : blockIdx.x;
-      const int total = runs ? a.run_first[blockIdx.x + 1] : a.head->items * a.Hkv;
+      const int total = runs ? a.run_first[blockIdx.x + 1] : units * a.Hkv;
       int kg = 0, q_uses[2] = {0, 0};
       bool ok = true;
       for (int i = 0; ok; ++i) {
         const int sl = i & 1;
         const bool more = idx < total;
         PlanItem it{};
-        if (more) it = load_item(a.items + (runs ? idx : idx / a.Hkv));
+        if (more) {
+          // (Without a list, the last units first: when causal, a sequence's
+          // last are its longest.)
+          if (direct)
+            it = direct_item(a, units - 1 - idx / a.Hkv, lane);
+          else
+            it = load_item(a.items + (runs ? idx : idx / a.Hkv));
+        }
         const int kvh = runs ? it.kvh : idx % a.Hkv;
         if (i >= 2 && !all(wait_bar(&bars->item_empty[sl], ((i >> 1) - 1) & 1, w))) break;
         int after = 0;
@@ -300,7 +362,7 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, PkCfg<D>::kMinBlocks)
           bars->item[sl][1] = make_int4(it.j0, it.j1, it.slot, it.seq);
           bars->kvh[sl] = kvh;
           mbar_arrive(&bars->item_full[sl]);
-          if (more && !runs) after = atomicAdd(&a.head->taken, 1);  // arrives while this item's tiles load
+          if (more && !runs && !direct) after = atomicAdd(&a.head->taken, 1);  // arrives while this item's tiles load
         }
         if (!more) break;
         const Unit x = make_unit<T>(it, kvh, a.TT, a.causal);
@@ -332,7 +394,7 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, PkCfg<D>::kMinBlocks)
           }
           if (!ok) break;
         }
-        idx = runs ? idx + 1 : gridDim.x + __shfl_sync(0xffffffffu, after, 0);
+        idx = runs ? idx + 1 : (direct ? idx + gridDim.x : gridDim.x + __shfl_sync(0xffffffffu, after, 0));
       }
       // Every copy issued must land before the CTA may exit.
 #pragma unroll
@@ -860,6 +922,7 @@ struct Layout {
   PlanLayout plan;
   int TT, unit;
   bool runs;            // the work may be cut into runs
+  bool direct;          // no list
   int max_parts;
   long long max_items;
   size_t off_o, off_l, bytes;
@@ -892,6 +955,10 @@ Layout make_layout(const SeqShape& s, const CacheShape* c, int ctas) {
     x.max_parts = most < 2 * grid ? static_cast<int>(most) : 2 * grid;
     x.max_items += kRunUnits + grid;
   }
+  // At most two items per CTA: finding them in the offsets costs a CTA less
+  // than the list's kernel before it (one prompt of 512 tokens, 8 + 1 heads, d =
+  // 64: 12.2 -> 11.2 us; of 1054, 32 + 16 heads: 21.6 -> 18.9).
+  x.direct = !c && !x.runs && x.max_items * s.Hkv <= 2 * grid && s.S <= kPlanSeqs;
   x.plan = plan_layout(x.max_items, x.runs ? grid : 0, x.runs ? grid : 0);
   x.off_o = x.plan.bytes;
   x.off_l = x.off_o + static_cast<size_t>(x.max_parts) * tiles * kBM * s.d * 4;
@@ -966,6 +1033,14 @@ cudaError_t launch_t(const SeqShape& s, const CacheShape* c, const Layout& x, co
   a.ctl = ctl;
   long long grid = x.max_items * s.Hkv;
   if (x.runs || grid > static_cast<long long>(C::kMinBlocks) * sms) grid = static_cast<long long>(C::kMinBlocks) * sms;
+  a.direct = x.direct;
+  a.S = s.S;
+  a.unit = x.unit;
+  a.cu = s.cu;
+  if (x.direct) {
+    kern<<<static_cast<unsigned>(grid), C::kThreads, C::kSmemBytes, stream>>>(tq, tk, tv, to, tr, a);
+    return cudaGetLastError();
+  }
   packed_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   e = launch_dependent(kern, dim3(static_cast<unsigned>(grid)), C::kThreads, C::kSmemBytes, stream, tq, tk, tv, to, tr,
