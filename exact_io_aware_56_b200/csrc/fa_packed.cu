@@ -934,14 +934,16 @@ Layout make_layout(const SeqShape& s, const CacheShape* c, int ctas) {
   x.TT = kBM / s.r();
   x.unit = tiles * x.TT;
   x.max_items = plan_max_units(s.S, s.T, x.unit);
-  // Runs where there can be so few units (the plan decides), of prompts fewer
-  // than CTAs: their keys are no more than their queries, and the merge's launch
-  // costs a microsecond. The sums of their costs stay in 32 bits.
+  // Runs where there can be so few units (the plan decides); of prompts fewer
+  // than half the CTAs, as their keys are no more than their queries, and the
+  // plan's way to runs and the merge's launch cost 4 us even where no unit is cut
+  // (17 short prompts of 16 heads: 18.4 -> 22.5 us). The sums of their costs
+  // stay in 32 bits.
   const int grid = tiles == 2 ? ctas : 2 * ctas;
   const long long least = (static_cast<long long>(s.T) + x.unit - 1) / x.unit;
   const long long keys = c ? static_cast<long long>(c->max_pages) * c->page : s.T;
   const long long key_tiles = (keys + kBN - 1) / kBN + 1;
-  x.runs = s.S <= kPlanSeqs && least * s.Hkv < static_cast<long long>(c ? kRunUnits : grid) &&
+  x.runs = s.S <= kPlanSeqs && least * s.Hkv < static_cast<long long>(c ? kRunUnits : grid / 2) &&
            (key_tiles + 4) * kCostTile * kRunUnits < (1LL << 31);
   // (The plan's own condition, for the longest units that there can be.)
   const long long most_cost = kCostItem + kCostTile * key_tiles;
