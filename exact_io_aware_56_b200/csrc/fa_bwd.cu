@@ -404,9 +404,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // iteration of the unit.
     if (nq * kQT > N) {
       uint32_t land_par = 0;
+      // Waits for a head's other tiles, which take 1 to 2 us each.
+      const Watch w_head{&bars->abort, a.ctl.err, a.ctl.budget_ns + static_cast<uint64_t>(nqi) * 20000};
       for (int it = nqi - 1 - it0 % nqi; ok && it < n_it; it += nqi) {
         const int s = it % kQStages;
-        ok = __all_sync(0xffffffffu, wait_bar(&bars->q_land[s], (land_par >> s) & 1, w));
+        ok = __all_sync(0xffffffffu, wait_bar(&bars->q_land[s], (land_par >> s) & 1, w_head));
         if (!ok) break;
         land_par ^= 1u << s;
         const int first = N - (nq - 1) * kQT;

@@ -115,6 +115,7 @@ struct PkArgs {
   const int* cu;
   int sectors;  // o (and its residual) can be stored 32 bytes at a time
   float scale_log2, rescale_tau;
+  uint64_t item_ns;  // ample for the longest item that there can be
   LaunchCtl ctl;
 };
 
@@ -271,13 +272,15 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, PkCfg<D>::kMinBlocks)
   pdl_wait();
   const uint32_t tmem = bars->tmem_base;
   const Watch w{&bars->abort, a.ctl.err, a.ctl.budget_ns};
+  // Waits that last as long as an item, whose key tiles take microseconds each.
+  const Watch w_item{&bars->abort, a.ctl.err, a.ctl.budget_ns + a.item_ns};
   auto all = [](bool b) { return __all_sync(0xffffffffu, b); };
 
   // The i-th item of this CTA, from the producer; false: none is left, or a
   // wait gave up. Whole warp.
   auto next_unit = [&](int i, Unit& x) -> bool {
     const int s = i & 1;
-    if (!all(wait_bar(&bars->item_full[s], (i >> 1) & 1, w))) return false;
+    if (!all(wait_bar(&bars->item_full[s], (i >> 1) & 1, w_item))) return false;
     const int4 p = bars->item[s][0], q = bars->item[s][1];
     const int kvh = bars->kvh[s];
     __syncwarp();
@@ -355,7 +358,7 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, PkCfg<D>::kMinBlocks)
             it = load_item(a.items + (runs ? idx : idx / a.Hkv));
         }
         const int kvh = runs ? it.kvh : idx % a.Hkv;
-        if (i >= 2 && !all(wait_bar(&bars->item_empty[sl], ((i >> 1) - 1) & 1, w))) break;
+        if (i >= 2 && !all(wait_bar(&bars->item_empty[sl], ((i >> 1) - 1) & 1, w_item))) break;
         int after = 0;
         if (lane == 0) {
           bars->item[sl][0] = make_int4(it.base, it.n, it.off, it.tok0);
@@ -441,7 +444,7 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, PkCfg<D>::kMinBlocks)
         const int keys = max(0, x.keys(x.n - 1));
         if (keys == kBN) continue;
         const int s = (vg - 1) % VS;
-        if (!all(wait_bar(&bars->v_land[s], (land_par >> s) & 1, w))) break;
+        if (!all(wait_bar(&bars->v_land[s], (land_par >> s) & 1, w_item))) break;
         land_par ^= 1u << s;
 #pragma unroll
         for (int b = 0; b < C::kBoxes; ++b) {
@@ -924,7 +927,7 @@ struct Layout {
   bool runs;            // the work may be cut into runs
   bool direct;          // no list
   int max_parts;
-  long long max_items;
+  long long max_items, key_tiles;
   size_t off_o, off_l, bytes;
 };
 
@@ -942,7 +945,7 @@ Layout make_layout(const SeqShape& s, const CacheShape* c, int ctas) {
   const int grid = tiles == 2 ? ctas : 2 * ctas;
   const long long least = (static_cast<long long>(s.T) + x.unit - 1) / x.unit;
   const long long keys = c ? static_cast<long long>(c->max_pages) * c->page : s.T;
-  const long long key_tiles = (keys + kBN - 1) / kBN + 1;
+  const long long key_tiles = x.key_tiles = (keys + kBN - 1) / kBN + 1;
   x.runs = s.S <= kPlanSeqs && least * s.Hkv < static_cast<long long>(c ? kRunUnits : grid / 2) &&
            (key_tiles + 4) * kCostTile * kRunUnits < (1LL << 31);
   // (The plan's own condition, for the longest units that there can be.)
@@ -1032,6 +1035,7 @@ cudaError_t launch_t(const SeqShape& s, const CacheShape* c, const Layout& x, co
   a.causal = s.causal;
   a.scale_log2 = s.scale * 1.4426950408889634f;
   a.rescale_tau = resid.p ? kRescaleExact : kRescaleLazy;
+  a.item_ns = static_cast<uint64_t>(x.key_tiles) * 20000;
   a.ctl = ctl;
   long long grid = x.max_items * s.Hkv;
   if (x.runs || grid > static_cast<long long>(C::kMinBlocks) * sms) grid = static_cast<long long>(C::kMinBlocks) * sms;

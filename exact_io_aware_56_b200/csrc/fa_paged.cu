@@ -369,6 +369,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     int len = 0, last_b = -1;
     uint32_t land_par = 0;
+    // A tail may be the last of a long run, whose tiles take 1 to 2 us each.
+    const Watch w_run{&bars->abort, a.ctl.err, a.ctl.budget_ns + static_cast<uint64_t>(start.t_hi - t_lo) * 20000};
     for (Cursor ta = start; !ta.done(); ta.next(a)) {
       if (ta.b != last_b) {
         last_b = ta.b;
@@ -377,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int keys = max(0, min(kT, len - ta.j * kT));
       if (keys == kT) continue;
       const int s = static_cast<int>(ta.t - t_lo) % ST;
-      if (!all(wait_bar(&bars->v_land[s], (land_par >> s) & 1, w))) break;
+      if (!all(wait_bar(&bars->v_land[s], (land_par >> s) & 1, w_run))) break;
       land_par ^= 1u << s;
       // A 128-byte row's 16-byte pieces stay within it under the swizzle.
 #pragma unroll

@@ -2,11 +2,15 @@
 //
 // The sequences' offsets live on the device, so that captured graphs can be
 // replayed on other lengths; what the host knows are the rows T and the
-// number of sequences S. A one-block kernel lists the work: `unit` tokens of
-// a sequence per item, longest items first (a counting sort by key tiles or
-// loop length in shared memory, so that the last wave is short), and the main kernel's CTAs,
-// launched for the largest possible count, leave when their item does not
-// exist.
+// number of sequences S. One block lists the work: `unit` tokens of a sequence
+// per item, longest items first (a counting sort by key tiles or loop length
+// in shared memory, so that the last wave is short). The forward's CTAs are
+// resident and take items until none is left; the backward's, launched for the
+// largest possible count, leave when their item does not exist.
+//
+// Few units leave most CTAs idle. The forward then cuts the whole work into one
+// run per CTA (units cut by a run's end leave partial results), the backward
+// each unit into parts of its steps.
 #pragma once
 
 #include "fa_internal.h"

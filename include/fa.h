@@ -356,7 +356,7 @@ int fa_packed_bwd(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa
  *   k_pages, v_pages [n_pages][Hkv][page_size][d]; key j of sequence b is slot
  *     j % page_size of page block_table[b * table_stride + j / page_size].
  *     Pages may be shared between sequences. Slots behind a sequence's end
- *     may hold anything, NaN included.
+ *     may hold anything, NaN included; before it, as in fa_packed_fwd.
  *   block_table int32 [S][max_pages] (rows table_stride apart); entries past
  *     a sequence's last page are not read.
  *   seq_lens int32 [S], 0 <= seq_lens[b] <= max_pages * page_size

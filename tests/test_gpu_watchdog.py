@@ -60,3 +60,27 @@ def test_paged_waits_time_out_cleanly_and_context_recovers(code, new, d):
     assert fa.fa_check_device_error() == fa.FA_OK
     assert_forward(o, lse, *oracle.paged_ref(to_f64(q), to_f64(cache.k), to_f64(cache.v), cache.table,
                                              np.asarray(cache.lens), offsets([new, new]), True, 0.125))
+
+
+def test_long_items_do_not_run_into_the_wait_limit():
+    """The warps that wait for an item's end wait as long as its tiles take: 1024 tiles, over a millisecond."""
+    from .packed import normal
+
+    T = 128 * 1024 - 1
+    q, k, v, dout = (normal(25 + i, T, 1, 64).cuda() for i in range(4))
+    cu = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+
+    def run():
+        o, lse = fa.attention_packed_forward(q, k, v, cu, False)
+        return o, lse, *fa.attention_packed_backward(q, k, v, o, dout, lse, cu, False)[1:]
+
+    want = run()
+    assert fa.fa_check_device_error() == fa.FA_OK
+    fa.fa_set_watchdog_ns(1_000_000)
+    try:
+        got = run()
+        assert fa.fa_check_device_error() == fa.FA_OK
+    finally:
+        fa.fa_set_watchdog_ns(2_000_000_000)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
