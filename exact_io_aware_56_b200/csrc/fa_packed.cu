@@ -1000,7 +1000,6 @@ cudaError_t launch_t(const SeqShape& s, const CacheShape* c, const Layout& x, co
   p.causal = s.causal;
   p.heads = s.Hkv;
   p.run_ctas = x.runs ? C::kMinBlocks * sms : 0;
-  p.half = C::T == 2 ? x.TT : 0;
   p.run_first = reinterpret_cast<int*>(ws + x.plan.run_first);
   p.sorted = x.max_items * s.Hkv > static_cast<long long>(C::kMinBlocks) * sms;
   p.head = reinterpret_cast<PlanHeader*>(ws + x.plan.head);

@@ -43,7 +43,6 @@ struct PlanArgs {
   int backward;    // items are key tiles of the backward, else query tokens of the forward
   int heads;       // CTAs per item (KV heads)
   int run_ctas;    // > 0: the work may be cut into this many runs
-  int half;        // units of at most this many tokens take less time (0: none)
   int r;           // backward: query heads of a KV head, gone through one after another
   int part_ctas;   // backward: > 0: units may be cut into parts for this many CTAs
   int sorted;      // 0: every CTA is resident at once, any order does
@@ -58,9 +57,10 @@ constexpr int kPlanSeqs = 1024;    // sequences held in shared memory at a time
 constexpr int kPlanBuckets = 1024;
 // Units of more parts than this are merged by more warps.
 constexpr int kMergeManyParts = 8;
-// Backward: units times KV heads below which units may be cut into parts, for
-// how many waves of CTAs at most, the least steps of a part, and what a CTA's
-// start and end take, in steps.
+// Backward: units times KV heads below which units may be cut into parts (at 304,
+// a training step of 2048 tokens, 16 + 16 heads, d = 64, the additions cost more
+// than a shorter last wave gains: 58.3 -> 61.6 us), for how many waves of CTAs at
+// most, the least steps of a part, and what a CTA's start and end take, in steps.
 constexpr int kPartUnits = 256;
 constexpr int kPartWaves = 3;
 constexpr int kPartLeast = 6;
@@ -68,10 +68,12 @@ constexpr int kPartSteps = 5;
 // Runs are made of fewer units times KV heads than this; more units are
 // balanced well enough by taking them longest first (4 per CTA).
 constexpr int kRunUnits = 4 * 148;
-// Cost of a key tile of a whole unit (two query tiles), of a unit of one query
-// tile, and of starting and ending an item, in quarters of a tile (measured
-// at d = 128: 1.7 us a tile, 4 us an item, part of it beside its neighbours).
-constexpr int kCostTile = 4, kCostHalf = 3, kCostItem = 6;
+// Cost of a key tile, and of starting and ending an item, in quarters of a tile
+// (measured at d = 128: 1.9 us a tile, 1.8 where only one of the two query tiles
+// has tokens; 4 us an item. With one query tile's taken for three quarters and
+// an item for 1.5 tiles, the last CTAs of a mix of chunks and single tokens
+// ended at 153 us, the mean one at 129: 158.5 -> 147 us for the call).
+constexpr int kCostTile = 4, kCostItem = 8;
 // No run is shorter than this (about six key tiles), so that few units are not
 // cut into more parts than their merge is worth; and no run end cuts off less
 // than kRunLeast key tiles of a unit.
@@ -226,7 +228,7 @@ __device__ void plan_block(const PlanArgs& a, PlanShared& sh) {
       if (u < U) {
         PlanItem it;
         const int w = unit_of(0, u, it);
-        cost = kCostItem + w * (it.n - it.tok0 <= a.half ? kCostHalf : kCostTile);
+        cost = kCostItem + w * kCostTile;
       }
       const int x = plan_scan<NT>(cost, sh.warp_sum, sum);
       if (u < U) sh.upos[u + 1] = total + x;
@@ -251,12 +253,11 @@ __device__ void plan_block(const PlanArgs& a, PlanShared& sh) {
           it.kvh = q - u * a.heads;
           const int cost = sh.upos[u + 1] - sh.upos[u];
           const int at = sh.upos[u] * a.heads + it.kvh * cost;
-          const int per = it.n - it.tok0 <= a.half ? kCostHalf : kCostTile;
           // Key tile at which run r ends within this unit.
           auto end_tile = [&](int r) {
             const int x = (r + 1) * len - at;
             if (x >= cost) return w;
-            const int j = (x - kCostItem) / per;
+            const int j = (x - kCostItem) / kCostTile;
             return j < kRunLeast ? 0 : (j > w - kRunLeast ? w : j);
           };
           int parts = 0, done = 0;
