@@ -264,6 +264,10 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, PkCfg<D>::kMinBlocks)
     tmem_alloc(&bars->tmem_base, C::kTmemCols);
     tmem_relinquish();
   }
+  // Without a list: the units, their loads beside the setup above.
+  const bool direct = !PAGED && a.direct;
+  int units = 0;
+  if (direct && warp == C::kProducerWarp) units = direct_units(a, lane);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -334,13 +338,7 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, PkCfg<D>::kMinBlocks)
       // Items of the list times the KV heads, taken one by one; or, where the
       // plan cut the work into runs, this CTA's own items.
       const bool runs = RUNS && a.head->runs != 0;
-      const bool direct = !PAGED && a.direct;
-      int units = 0;
-      if (direct) {
-        units = direct_units(a, lane);
-      } else {
-        units = a.head->items;
-      }
+      if (!direct) units = a.head->items;
       int idx = runs ? a.run_first[blockIdx.x] : blockIdx.x;
       const int total = runs ? a.run_first[blockIdx.x + 1] : units * a.Hkv;
       int kg = 0, q_uses[2] = {0, 0};
