@@ -159,9 +159,49 @@ __device__ __forceinline__ int direct_units(const PkArgs& a, int lane) {
   return __reduce_add_sync(0xffffffffu, n);
 }
 
-// Unit u of them, by the whole warp: 32 sequences a step.
-__device__ __forceinline__ PlanItem direct_item(const PkArgs& a, int u, int lane) {
+// Units of a sequence of n tokens that take fewer than w key tiles.
+__device__ __forceinline__ int direct_less(const PkArgs& a, int n, int w) {
+  if (n <= (w - 1) * kBN) return (n + a.unit - 1) / a.unit;
+  return a.causal ? (w - 1) * kBN / a.unit : 0;
+}
+
+// The unit of this rank, by the whole warp. Where some CTAs take two units, of
+// up to 32 sequences, one per lane: rank 0 takes the most key tiles; w, the
+// rank's, by bisection of the number of units that take w or more. (17 short
+// prompts of 16 heads, where a CTA's second unit could be one of the longest:
+// 14.8 -> 13.5 us; the search itself costs 0.5 to 1 us.) Else, or of more
+// sequences, which are shorter then: the last unit first, 32 sequences a step.
+__device__ __forceinline__ PlanItem direct_item(const PkArgs& a, int units, int rank, int lane) {
   PlanItem it{};
+  if (a.S <= 32 && units * a.Hkv > static_cast<int>(gridDim.x)) {
+    SeqRange s{};
+    if (lane < a.S) s = seq_range(a.cu, nullptr, lane, a.total, a.total, a.total);
+    const int mine = (s.n + a.unit - 1) / a.unit;
+    int w = 1, hi = (__reduce_max_sync(0xffffffffu, s.n) + kBN - 1) / kBN;
+    int longer = 0;  // units of more than w key tiles
+    while (w < hi) {
+      const int mid = (w + hi + 1) / 2;
+      const int n = __reduce_add_sync(0xffffffffu, mine - direct_less(a, s.n, mid));
+      if (n > rank) {
+        w = mid;
+      } else {
+        hi = mid - 1;
+        longer = n;
+      }
+    }
+    const int first = direct_less(a, s.n, w);
+    const int same = direct_less(a, s.n, w + 1) - first;
+    int end = same;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, end, o);
+      if (lane >= o) end += y;
+    }
+    const int l = __ffs(__ballot_sync(0xffffffffu, end > rank - longer)) - 1;
+    const int tok0 = (__shfl_sync(0xffffffffu, first + same - end, l) + rank - longer) * a.unit;
+    return PlanItem{__shfl_sync(0xffffffffu, s.start, l), __shfl_sync(0xffffffffu, s.n, l), 0, tok0, 0, w, -1, l, -1};
+  }
+  const int u = units - 1 - rank;
   int before = 0;
   for (int b0 = 0; b0 < a.S; b0 += 32) {
     SeqRange s{};
@@ -348,10 +388,8 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, PkCfg<D>::kMinBlocks)
         const bool more = idx < total;
         PlanItem it{};
         if (more) {
-          // (Without a list, the last units first: when causal, a sequence's
-          // last are its longest.)
           if (direct)
-            it = direct_item(a, units - 1 - idx / a.Hkv, lane);
+            it = direct_item(a, units, idx / a.Hkv, lane);
           else
             it = load_item(a.items + (runs ? idx : idx / a.Hkv));
         }
@@ -395,7 +433,14 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, PkCfg<D>::kMinBlocks)
           }
           if (!ok) break;
         }
-        idx = runs ? idx + 1 : (direct ? idx + gridDim.x : gridDim.x + __shfl_sync(0xffffffffu, after, 0));
+        // (Without a list there are at most two items per CTA: the longest of the
+        // second ones go to the CTAs of the shortest first ones.)
+        if (runs)
+          ++idx;
+        else if (direct)
+          idx = i > 0 ? total : 2 * gridDim.x - 1 - idx;
+        else
+          idx = gridDim.x + __shfl_sync(0xffffffffu, after, 0);
       }
       // Every copy issued must land before the CTA may exit.
 #pragma unroll
