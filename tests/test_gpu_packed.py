@@ -218,6 +218,31 @@ def test_captured_training_step_replays_on_other_lengths():
         backward_check(*host, out[2:], c, True, 0.125)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("d,heads", [(64, 18), (128, 12)])
+def test_two_units_for_some_ctas(d, heads, causal):
+    # More units than CTAs, fewer than twice as many: first units taken by length, second ones in turn. Replayed on
+    # lengths of one unit per CTA and of a single sequence.
+    lens = [300, 1, 77, 128, 129, 255, 64, 33, 2, 190, 256, 17, 0, 100]
+    q, k, v, _ = inputs(lens, heads, heads, d, 141)
+    cu = torch.from_numpy(offsets(lens)).cuda()
+    qd, kd, vd = q.cuda(), k.cuda(), v.cuda()
+    fa.attention_packed_forward(qd, kd, vd, cu, causal, 0.125)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        o, lse = fa.attention_packed_forward(qd, kd, vd, cu, causal, 0.125)
+    for c in (lens, [128, 256, 384, 700] + [0] * 10, [0] * 13 + [sum(lens)]):
+        c = offsets(c)
+        assert c[-1] <= q.shape[0]
+        cu.copy_(torch.from_numpy(c))
+        g.replay()
+        done()
+        ref = oracle.packed_fwd_ref(to_f64(q), to_f64(k), to_f64(v), c, causal, 0.125)
+        rows = slice(0, c[-1])
+        assert_forward(o[rows], lse[:, rows], *(x[:, rows] if i == 1 else x[rows] for i, x in enumerate(ref)))
+
+
 def test_many_sequences():
     # More sequences than the list's one-block kernel has threads, most of them empty or short.
     rng = np.random.default_rng(7)
