@@ -37,7 +37,8 @@
 // [384,...) O_0 (, O_1 at d = 64). The ordering argument is fa_decode.cu's:
 // S_(j+1) is issued before P_j V_j, so a complete S_(j+1) means that the P
 // buffer it pairs with is free; O is rescaled only after pv_done of the
-// previous tile.
+// previous tile; p_ready is a barrier per tile parity, as a fast warp arrives
+// for tile j + 1 before a slow one has for tile j.
 
 #include <cuda_bf16.h>
 #include <math_constants.h>
@@ -93,7 +94,7 @@ struct Args {
 struct Bars {
   uint64_t q_full[2], q_empty[2];
   uint64_t k_full[6], v_full[6], v_land[6], kv_empty[6];
-  uint64_t s_full[2], p_ready, pv_done;
+  uint64_t s_full[2], p_ready[2], pv_done;
   uint64_t o_full[2], o_empty[2];
   uint64_t drain;
   uint32_t tmem_base;
@@ -237,6 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars->o_full[b], 1);
       mbar_init(&bars->o_empty[b], kT);
       mbar_init(&bars->s_full[b], 1);
+      mbar_init(&bars->p_ready[b], kT);
     }
     for (int s = 0; s < ST; ++s) {
       mbar_init(&bars->k_full[s], 1);
@@ -244,7 +246,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars->v_land[s], 1);
       mbar_init(&bars->kv_empty[s], 1);
     }
-    mbar_init(&bars->p_ready, kT);
     mbar_init(&bars->pv_done, 1);
     mbar_init(&bars->drain, 1);
     bars->abort = 0;
@@ -426,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int g = static_cast<int>(ta.t - t_lo);
         const int s = g % ST;
         const int ob = ta.e % OB;
-        if (!all(wait_bar(&bars->p_ready, g & 1, w)) || !all(wait_bar(&bars->v_full[s], (g / ST) & 1, w))) return false;
+        if (!all(wait_bar(&bars->p_ready[g & 1], (g >> 1) & 1, w)) || !all(wait_bar(&bars->v_full[s], (g / ST) & 1, w))) return false;
         const bool first = ta.first();
         if (first && ta.e >= OB && !all(wait_bar(&bars->o_empty[ob], ((ta.e / OB) - 1) & 1, w))) return false;
         tc_fence_after();
@@ -586,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       l += sum;
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(&bars->p_ready);
+      mbar_arrive(&bars->p_ready[g & 1]);
       if (ta.last()) {
         if (!all(wait_bar(&bars->o_full[ob], (ta.e / OB) & 1, w))) break;
         tc_fence_after();

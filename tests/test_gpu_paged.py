@@ -391,3 +391,36 @@ def test_large_and_rising_scores(new, d):
     w = weight_error(q, cache.k.nan_to_num(0.0).flatten(0, 1).flatten(0, 1)[:, None], scale)
     assert_within("O", o, O, w * A + HALF * np.abs(O) + 1e-6)
     assert_within("L", lse, L, (w - HALF) + 2.0 ** -22 * np.abs(L))
+
+
+@pytest.mark.parametrize("new", [1, 8, 16])
+@pytest.mark.parametrize("d", [64, 128])
+def test_few_rows_repeat_where_warps_differ(new, d):
+    # Four, two and one copies of 4, 64 and 128 rows, about 14 key tiles in a row per CTA. Scores of some warps' rows
+    # rise from tile to tile by 4 in all, those of the others fall, so that some warps rescale O at most tiles and the
+    # others, which run ahead of them, at none.
+    S, n, page, hkv, r = 16, 4096, 64, 4, 4 if new == 1 else 8
+    k, v = normal(101, n, hkv, d).float() / 2, normal(102, n, hkv, d)
+    j = torch.arange(n)
+    rise = 32.0 * (j // 128) / (n // 128 - 1)
+    k[:, :, 0] = (rise if new == 16 else torch.where(j % 128 < 64, rise, -rise))[:, None]
+    q = normal(103, S, new, hkv, r, d)
+    row = torch.arange(new * r).view(new, r)
+    q[..., 0] = torch.where(row // 32 % 2 == 0, 1.0, -1.0)[:, None].to(torch.bfloat16)
+    q = q.view(S * new, hkv * r, d)
+    # All sequences share the pages of one, and end at different keys.
+    order = torch.from_numpy(np.random.default_rng(104).permutation(n // page).astype(np.int32))
+    kp, vp = (torch.empty(n // page, hkv, page, d, dtype=torch.bfloat16) for _ in range(2))
+    for pages, x in ((kp, k.to(torch.bfloat16)), (vp, v)):
+        pages[order.long()] = x.view(n // page, page, hkv, d).transpose(1, 2)
+    table = order[None].repeat(S, 1)
+    lens = np.array([n - 37 * b for b in range(S)], dtype=np.int32)
+    cu = offsets([new] * S)
+    args = [x.cuda() for x in (q, kp, vp, table, torch.from_numpy(lens), torch.from_numpy(cu))]
+    first = None
+    for _ in range(100):
+        got = fa.attention_paged(*args, new, True, 0.125)
+        first = first or got
+        assert torch.equal(got[0], first[0]) and torch.equal(got[1], first[1])
+    done()
+    assert_forward(*first, *oracle.paged_ref(to_f64(q), to_f64(kp), to_f64(vp), table.numpy(), lens, cu, True, 0.125))
