@@ -50,6 +50,9 @@
 // P_j V_j while the softmax works on tile j+1, so a warp that must rescale
 // O first waits for the pv_done phase of tile j (P_(j+1) V_(j+1) cannot
 // start before this warp hands P_(j+1) back, so that phase is unambiguous).
+// A warp that does not rescale waits for S_(j+1) only and may arrive for it
+// before a slow warp has for tile j, hence a p_ready barrier per tile parity;
+// S_(j+2) is issued after p_ready of tile j, so no warp leads by two tiles.
 
 #include <cuda_bf16.h>
 #include <math_constants.h>
@@ -80,7 +83,7 @@ struct DecCfg {
   static constexpr int kOffK = kQBufs * kTileBytes;
   static constexpr int kOffV = kOffK + kStages * kTileBytes;
   static constexpr int kOffBar = kOffV + kStages * kTileBytes;
-  static constexpr int kSmemBytes = kOffBar + 256 + 1024;  // + alignment slack
+  static constexpr int kSmemBytes = kOffBar + 320 + 1024;  // + alignment slack
   static constexpr uint32_t kTmemCols = 512;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
   static_assert(kColO + kOBufs * D <= kTmemCols, "tensor memory budget");
@@ -98,13 +101,13 @@ struct DecArgs {
 struct DecBars {
   uint64_t q_full[2], q_empty[2];
   uint64_t k_full[6], v_full[6], kv_empty[6];
-  uint64_t s_full[2], p_ready, pv_done;
+  uint64_t s_full[2], p_ready[2], pv_done;
   uint64_t o_full[2], o_empty[2];
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
 };
-static_assert(sizeof(DecBars) <= 256, "barrier block exceeds its shared-memory reservation");
+static_assert(sizeof(DecBars) <= 320, "barrier block exceeds its shared-memory reservation");
 
 // Walks the tiles of this CTA's run [t_lo, t_hi) in order, tracking the
 // unit u, its segment e (0 = the run's first unit) and tile j of the unit
@@ -157,13 +160,13 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       mbar_init(&bars->o_full[b], 1);
       mbar_init(&bars->o_empty[b], kT);
       mbar_init(&bars->s_full[b], 1);
+      mbar_init(&bars->p_ready[b], kT);
     }
     for (int s = 0; s < ST; ++s) {
       mbar_init(&bars->k_full[s], 1);
       mbar_init(&bars->v_full[s], 1);
       mbar_init(&bars->kv_empty[s], 1);
     }
-    mbar_init(&bars->p_ready, kT);
     mbar_init(&bars->pv_done, 1);
     mbar_init(&bars->drain, 1);
     bars->abort = 0;
@@ -272,7 +275,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         const int g = static_cast<int>(ta.t - t_lo);
         const int s = g % ST;
         const int ob = ta.e % OB;
-        if (!all(wait_bar(&bars->p_ready, g & 1, w)) || !all(wait_bar(&bars->v_full[s], (g / ST) & 1, w))) return false;
+        if (!all(wait_bar(&bars->p_ready[g & 1], (g >> 1) & 1, w)) || !all(wait_bar(&bars->v_full[s], (g / ST) & 1, w))) return false;
         const bool first = ta.first(t_lo);
         if (first && ta.e >= OB && !all(wait_bar(&bars->o_empty[ob], ((ta.e / OB) - 1) & 1, w))) return false;
         tc_fence_after();
@@ -428,7 +431,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       l += sum;
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(&bars->p_ready);
+      mbar_arrive(&bars->p_ready[g & 1]);
       if (ta.last()) {
         if (!__all_sync(0xffffffffu, wait_bar(&bars->o_full[ob], (ta.e / OB) & 1, w))) break;
         tc_fence_after();

@@ -151,3 +151,33 @@ def test_decode_argument_errors():
     with pytest.raises(fa.FaError):
         fa.fa_decode(q, dev["k"], dev["v"], torch.empty_like(q), torch.empty(1, 4, 65, device="cuda"), True,
                      0.125, torch.empty(1 << 20, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("r,Nq", [(4, 1), (8, 8), (8, 16)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_repeats_where_warps_differ(r, Nq, d):
+    # Four, two and one copies of 4, 64 and 128 rows, about 14 key tiles in a row per CTA. Scores of some warps' rows
+    # rise from tile to tile by 4 in all, those of the others fall, so that some warps rescale O at most tiles and the
+    # others, which run ahead of them, at none.
+    B, Hkv, Nk, scale = 16, 4, 4096, 0.125
+    host = make_decode_inputs(B, r * Hkv, Hkv, Nq, Nk, d, 900 + Nq)
+    j, row = torch.arange(Nk), torch.arange(r * Nq).view(r, Nq)
+    rise = 32.0 * (j // 128) / (Nk // 128 - 1)
+    if r * Nq <= 64:
+        rise = torch.where(j % 128 < 64, rise, -rise)
+    host["k"][..., 0] = rise.to(torch.bfloat16)
+    host["q"].view(B, Hkv, r, Nq, d)[..., 0] = torch.where(row // 32 % 2 == 0, 1.0, -1.0).to(torch.bfloat16)
+    dev = {k: t.cuda() for k, t in host.items()}
+    first = None
+    for _ in range(100):
+        got = fa.attention_decode(dev["q"], dev["k"], dev["v"], True, scale)
+        first = first or got
+        assert torch.equal(got[0], first[0]) and torch.equal(got[1], first[1])
+    torch.cuda.synchronize()
+    assert fa.fa_check_device_error() == fa.FA_OK
+    ref = {k: to_f64(t) for k, t in host.items()}
+    O, L = oracle.attn_decode_ref(ref["q"], ref["k"], ref["v"], scale, True)
+    # The weights are rounded to bf16 (half a step, 2^-8 of each) and a further 2^-11 off by their exponents' error; so
+    # is O to bf16. L by the error of S: 128 products in fp32, at most 128 * 2^-24 * scale * sum |q k| (below 22).
+    assert (np.abs(to_f64(first[0]) - O) <= (2.0 ** -8 + 2.0 ** -11) * np.abs(ref["v"]).max() + 2.0 ** -8 * np.abs(O)).all()
+    assert (np.abs(to_f64(first[1]) - L) <= 128 * 2.0 ** -24 * 22 + 1e-5).all()
