@@ -612,6 +612,11 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, PkCfg<D>::kMinBlocks)
       const int nt = T == 2 && t == 1 ? x.n_t[1] : x.n_t[0];
       const int tok0 = T == 2 && t == 1 ? x.tok_t[1] : x.tok_t[0];
       const int tok = tok0 + rw_tok;
+      // Rows of other sequences, and rows that no token fills (128 % r of them,
+      // whatever shared memory held), have no say in when O is rescaled:
+      // results would depend on what lies beside a sequence.
+      const bool mine = rw < a.TT * a.r && tok < x.it.n;
+      const float tau = mine ? a.rescale_tau : CUDART_INF_F;
       // Last visible key of this row, and of the tile's first.
       const int lim = a.causal ? min(x.it.off + tok, x.len() - 1) : x.len() - 1;
       const int lim0 = a.causal ? min(x.it.off + tok0, x.len() - 1) : x.len() - 1;
@@ -650,7 +655,7 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, PkCfg<D>::kMinBlocks)
         float alpha = 1.f;
         if (u == 0) {
           m = m_cand;  // -inf for a row that sees no key of this tile
-        } else if (__any_sync(0xffffffffu, m_cand > m + a.rescale_tau)) {
+        } else if (__any_sync(0xffffffffu, m_cand > m + tau)) {
           const float m_new = fmaxf(m, m_cand);
           alpha = m_new == -CUDART_INF_F ? 1.f : exp2_accurate(m - m_new);
           m = m_new;
@@ -719,7 +724,6 @@ __global__ void __launch_bounds__(PkCfg<D>::kThreads, PkCfg<D>::kMinBlocks)
       }
       if (!ok) break;
       tc_fence_after();
-      const bool mine = rw < a.TT * a.r && tok < x.it.n;
       const float inv_l = l == 0.f ? 0.f : 1.f / l;  // 0: no visible key (O is 0 there, or never written)
       const float L = l == 0.f ? -CUDART_INF_F : (m + lg2(l)) * 0.69314718055994530942f;
       const long long row = static_cast<long long>(x.it.base) + tok;

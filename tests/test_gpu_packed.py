@@ -327,3 +327,44 @@ def test_saturated_rows_are_exact():
     assert torch.equal(o.cpu(), v[torch.from_numpy(pick), torch.from_numpy(heads)[None]])
     assert (lse.cpu().t() / (0.125 * 64 * d) - 1).abs().max() < 2e-6
     assert (r == 0).all()
+
+
+@pytest.mark.parametrize("r", [3, 5, 7])
+@pytest.mark.parametrize("d", [64, 128])
+def test_groups_that_leave_rows_of_a_tile_free_repeat(d, r):
+    # 128 % r rows of a query tile belong to no token. Whatever another call left in shared memory there (zeros, or
+    # queries with scores of hundreds), the results are the same bits.
+    lens, hkv = [700, 300, 129], 4
+    q, k, v, _ = (x.cuda() for x in inputs(lens, r * hkv, hkv, d, 500 + r))
+    cu = torch.from_numpy(offsets(lens)).cuda()
+    other = normal(510, 8192, 16, d).cuda()
+    whole = torch.tensor([0, 4096, 8192], dtype=torch.int32, device="cuda")
+    pages = [x.view(-1, 16, hkv, d).transpose(1, 2).contiguous() for x in (k[:1024], v[:1024])]
+    table, ln = torch.arange(64, dtype=torch.int32, device="cuda").view(2, 32), torch.tensor([500, 400], dtype=torch.int32, device="cuda")
+    new = torch.from_numpy(offsets([200, 130])).cuda()
+    got = []
+    for gain in (0.0, 100.0, 0.0, -100.0):
+        fa.attention_packed_forward(other * gain, other, other, whole, False, 0.125)
+        got.append(fa.attention_packed_forward(q, k, v, cu, True, 0.125))
+        fa.attention_packed_forward(other * gain, other, other, whole, False, 0.125)
+        got[-1] += fa.attention_paged(q[:330], *pages, table, ln, new, 200, True, 0.125)
+    done()
+    for x in got[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(x, got[0]))
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("d,hq,hkv", [(64, 4, 4), (64, 8, 2), (128, 4, 4), (128, 8, 2)])
+def test_a_neighbours_queries_change_no_bit(d, hq, hkv, causal):
+    # The first sequence's last query tile also holds the second one's first queries, of large scores or none.
+    lens = [300, 300]
+    q, k, v, _ = (x.cuda() for x in inputs(lens, hq, hkv, d, 520))
+    cu = torch.from_numpy(offsets(lens)).cuda()
+    got = []
+    for gain in (0.0, 100.0, 1.0):
+        x = q.clone()
+        x[300:] *= gain
+        got.append(fa.attention_packed_forward(x, k, v, cu, causal, 0.125))
+    done()
+    for o, lse in got[1:]:
+        assert torch.equal(o[:300], got[0][0][:300]) and torch.equal(lse[:, :300], got[0][1][:, :300])
