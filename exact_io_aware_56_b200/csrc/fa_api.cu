@@ -432,10 +432,6 @@ void fa_set_watchdog_ns(uint64_t ns) { g_budget_ns.store(ns < 1000000ull ? 10000
 
 // ------------------------------------------ packed sequences, paged cache
 
-// At most this many CTAs share the work that is cut along the keys (one per
-// SM of a B200); the workspace sizes depend on it.
-static constexpr int kShareCtas = 148;
-
 // Strides: whole 16-byte pieces, positive where there is more than one
 // element (a stride of zero would make rows share memory), and below TMA's
 // 2^40 bytes.
@@ -473,7 +469,7 @@ static int check_cache(int n_pages, int page_size, int max_pages, int max_q) {
 
 size_t fa_packed_fwd_workspace_bytes(int S, int T, int Hq, int Hkv, int d) {
   if (check_seqs(S, T, Hq, Hkv, d, 0, 1.f) != FA_OK) return 0;
-  return packed_fwd_workspace_bytes(SeqShape{S, T, nullptr, Hq, Hkv, d, 0, 1.f}, nullptr, kShareCtas);
+  return packed_fwd_workspace_bytes(SeqShape{S, T, nullptr, Hq, Hkv, d, 0, 1.f}, nullptr);
 }
 
 int fa_packed_fwd(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa_rows* o, const fa_rows* o_resid,
@@ -487,7 +483,7 @@ int fa_packed_fwd(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa
       !workspace || !aligned16(workspace))
     return FA_ERR_INVALID_ARGUMENT;
   const SeqShape s{S, T, cu_seqlens, Hq, Hkv, d, causal, scale};
-  if (workspace_bytes < packed_fwd_workspace_bytes(s, nullptr, kShareCtas)) return FA_ERR_INVALID_ARGUMENT;
+  if (workspace_bytes < packed_fwd_workspace_bytes(s, nullptr)) return FA_ERR_INVALID_ARGUMENT;
   DevState* st = nullptr;
   if ((rc = device_state(&st)) != FA_OK) return rc;
   const int ctas = st->sms < kShareCtas ? st->sms : kShareCtas;
@@ -529,7 +525,7 @@ size_t fa_paged_fwd_workspace_bytes(int S, int T, int max_q, int Hq, int Hkv, in
   const SeqShape s{S, T, nullptr, Hq, Hkv, d, 0, 1.f};
   CacheShape c{0, page_size, max_pages, nullptr, nullptr, 0, max_q < T ? max_q : T};
   return paged_few_rows(s, c) ? paged_few_workspace_bytes(s, c, kShareCtas)
-                              : packed_fwd_workspace_bytes(s, &c, kShareCtas);
+                              : packed_fwd_workspace_bytes(s, &c);
 }
 
 int fa_paged_fwd(const fa_rows* q, const fa_pages* k_pages, const fa_pages* v_pages, const fa_rows* o, float* lse,
@@ -549,7 +545,7 @@ int fa_paged_fwd(const fa_rows* q, const fa_pages* k_pages, const fa_pages* v_pa
   const SeqShape s{S, T, cu_seqlens, Hq, Hkv, d, causal, scale};
   const CacheShape c{n_pages, page_size, max_pages, seq_lens, block_table, table_stride, max_q < T ? max_q : T};
   const bool few = paged_few_rows(s, c);
-  const size_t need = few ? paged_few_workspace_bytes(s, c, kShareCtas) : packed_fwd_workspace_bytes(s, &c, kShareCtas);
+  const size_t need = few ? paged_few_workspace_bytes(s, c, kShareCtas) : packed_fwd_workspace_bytes(s, &c);
   if (workspace_bytes < need) return FA_ERR_INVALID_ARGUMENT;
   DevState* st = nullptr;
   if ((rc = device_state(&st)) != FA_OK) return rc;
@@ -671,6 +667,17 @@ int fa_test_decode_plan(int B, int Hq, int Hkv, int Nq, int Nk, int d, int num_c
   const DecodePlan p = make_decode_plan(s, num_ctas);
   const long long v[8] = {p.W, p.T, p.G, p.MS, p.R, p.rho, p.rv, p.n_chunks};
   for (int i = 0; i < 8; ++i) out[i] = v[i];
+  return FA_OK;
+}
+
+int fa_test_packed_layout(int S, int T, int Hq, int Hkv, int d, int page_size, int max_pages, int num_sms,
+                          long long* out) {
+  if (!out || num_sms < 1) return FA_ERR_INVALID_ARGUMENT;
+  int rc = check_seqs(S, T, Hq, Hkv, d, 0, 1.f);
+  if (rc != FA_OK || (page_size != 0 && (rc = check_cache(0, page_size, max_pages, T)) != FA_OK)) return rc;
+  const SeqShape s{S, T, nullptr, Hq, Hkv, d, 0, 1.f};
+  const CacheShape c{0, page_size, max_pages, nullptr, nullptr, 0, T};
+  packed_fwd_layout(s, page_size ? &c : nullptr, num_sms < kShareCtas ? num_sms : kShareCtas, out);
   return FA_OK;
 }
 

@@ -203,6 +203,10 @@ cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, int threads, size_t 
   return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
 }
 
+// At most this many multiprocessors (a B200's) share the work that is cut along
+// the keys; the workspace sizes depend on it.
+constexpr int kShareCtas = 148;
+
 // True when every sequence's query rows of a KV head fit one 128-row tile:
 // these calls take the few-row kernel (fa_paged.cu), the others the prompt
 // kernel (fa_packed.cu).
@@ -227,7 +231,9 @@ struct alignas(16) PlanItem {
   int kvh;       // KV head, where the items carry it
 };
 
-size_t packed_fwd_workspace_bytes(const SeqShape& s, const CacheShape* c, int ctas);
+size_t packed_fwd_workspace_bytes(const SeqShape& s, const CacheShape* c);
+// For tests: see fa_test_packed_layout.
+void packed_fwd_layout(const SeqShape& s, const CacheShape* c, int sms, long long* out);
 cudaError_t launch_packed_fwd(const SeqShape& s, const CacheShape* c, const Rows& q, const Rows& o, const Rows& resid,
                               const Rows& krows, const Rows& vrows, const Pages& kpages, const Pages& vpages,
                               float* lse, void* workspace, int sms, const LaunchCtl& ctl, cudaStream_t stream);

@@ -975,10 +975,14 @@ struct Layout {
   bool direct;          // no list
   int max_parts;
   long long max_items, key_tiles;
+  long long grid;       // CTAs of the launch
   size_t off_o, off_l, bytes;
 };
 
-Layout make_layout(const SeqShape& s, const CacheShape* c, int ctas) {
+// What is laid out depends on the shape alone (kShareCtas, not the device's
+// multiprocessors), as the size queries know no more: the choice of runs is not
+// monotone in the CTAs. `sms`, at most kShareCtas, are those of the launch.
+Layout make_layout(const SeqShape& s, const CacheShape* c, int sms) {
   Layout x;
   const int tiles = s.d == 128 ? 2 : 1;
   x.TT = kBM / s.r();
@@ -989,29 +993,31 @@ Layout make_layout(const SeqShape& s, const CacheShape* c, int ctas) {
   // plan's way to runs and the merge's launch cost 4 us even where no unit is cut
   // (17 short prompts of 16 heads: 18.4 -> 22.5 us). The sums of their costs
   // stay in 32 bits.
-  const int grid = tiles == 2 ? ctas : 2 * ctas;
+  const int per_sm = tiles == 2 ? 1 : 2;
+  const int most_ctas = per_sm * kShareCtas, ctas = per_sm * sms;
   const long long least = (static_cast<long long>(s.T) + x.unit - 1) / x.unit;
   const long long keys = c ? static_cast<long long>(c->max_pages) * c->page : s.T;
   const long long key_tiles = x.key_tiles = (keys + kBN - 1) / kBN + 1;
-  x.runs = s.S <= kPlanSeqs && least * s.Hkv < static_cast<long long>(c ? kRunUnits : grid / 2) &&
+  x.runs = s.S <= kPlanSeqs && least * s.Hkv < static_cast<long long>(c ? kRunUnits : most_ctas / 2) &&
            (key_tiles + 4) * kCostTile * kRunUnits < (1LL << 31);
   // (The plan's own condition, for the longest units that there can be.)
   const long long most_cost = kCostItem + kCostTile * key_tiles;
-  const long long mean_cost = x.max_items * s.Hkv * most_cost / grid;
+  const long long mean_cost = x.max_items * s.Hkv * most_cost / most_ctas;
   if (!plan_wants_runs(mean_cost, most_cost)) x.runs = false;
   x.max_parts = 0;
   if (x.runs) {
     // Each run boundary adds an item and cuts at most one unit; the parts of a
     // unit are kRunLeast key tiles or more.
     const long long most = x.max_items * s.Hkv * (key_tiles / kRunLeast);
-    x.max_parts = most < 2 * grid ? static_cast<int>(most) : 2 * grid;
-    x.max_items += kRunUnits + grid;
+    x.max_parts = most < 2 * most_ctas ? static_cast<int>(most) : 2 * most_ctas;
+    x.max_items += kRunUnits + most_ctas;
   }
   // At most two items per CTA: finding them in the offsets costs a CTA less
   // than the list's kernel before it (one prompt of 512 tokens, 8 + 1 heads, d =
   // 64: 12.2 -> 11.2 us; of 1054, 32 + 16 heads: 21.6 -> 18.9).
-  x.direct = !c && !x.runs && x.max_items * s.Hkv <= 2 * grid && s.S <= kPlanSeqs;
-  x.plan = plan_layout(x.max_items, x.runs ? grid : 0, x.runs ? grid : 0);
+  x.direct = !c && !x.runs && x.max_items * s.Hkv <= 2 * ctas && s.S <= kPlanSeqs;
+  x.grid = x.runs || x.max_items * s.Hkv > ctas ? ctas : x.max_items * s.Hkv;
+  x.plan = plan_layout(x.max_items, x.runs ? most_ctas : 0, x.runs ? most_ctas : 0);
   x.off_o = x.plan.bytes;
   x.off_l = x.off_o + static_cast<size_t>(x.max_parts) * tiles * kBM * s.d * 4;
   x.bytes = x.off_l + static_cast<size_t>(x.max_parts) * tiles * kBM * 4 + 32;  // + alignment of the parts
@@ -1083,19 +1089,17 @@ cudaError_t launch_t(const SeqShape& s, const CacheShape* c, const Layout& x, co
   a.rescale_tau = resid.p ? kRescaleExact : kRescaleLazy;
   a.item_ns = static_cast<uint64_t>(x.key_tiles) * 20000;
   a.ctl = ctl;
-  long long grid = x.max_items * s.Hkv;
-  if (x.runs || grid > static_cast<long long>(C::kMinBlocks) * sms) grid = static_cast<long long>(C::kMinBlocks) * sms;
   a.direct = x.direct;
   a.S = s.S;
   a.unit = x.unit;
   a.cu = s.cu;
   if (x.direct) {
-    kern<<<static_cast<unsigned>(grid), C::kThreads, C::kSmemBytes, stream>>>(tq, tk, tv, to, tr, a);
+    kern<<<static_cast<unsigned>(x.grid), C::kThreads, C::kSmemBytes, stream>>>(tq, tk, tv, to, tr, a);
     return cudaGetLastError();
   }
   packed_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  e = launch_dependent(kern, dim3(static_cast<unsigned>(grid)), C::kThreads, C::kSmemBytes, stream, tq, tk, tv, to, tr,
+  e = launch_dependent(kern, dim3(static_cast<unsigned>(x.grid)), C::kThreads, C::kSmemBytes, stream, tq, tk, tv, to, tr,
                        a);
   if (e != cudaSuccess || !x.runs) return e;
   return launch_dependent(packed_merge_kernel<D>, dim3(8 * sms), 128, 0, stream, a);
@@ -1103,8 +1107,17 @@ cudaError_t launch_t(const SeqShape& s, const CacheShape* c, const Layout& x, co
 
 }  // namespace
 
-size_t packed_fwd_workspace_bytes(const SeqShape& s, const CacheShape* c, int ctas) {
-  return make_layout(s, c, ctas).bytes;
+size_t packed_fwd_workspace_bytes(const SeqShape& s, const CacheShape* c) {
+  return make_layout(s, c, kShareCtas).bytes;
+}
+
+void packed_fwd_layout(const SeqShape& s, const CacheShape* c, int sms, long long* out) {
+  const Layout x = make_layout(s, c, sms);
+  out[0] = static_cast<long long>(x.bytes);
+  out[1] = x.runs;
+  out[2] = x.direct;
+  out[3] = x.max_items * s.Hkv;
+  out[4] = x.grid;
 }
 
 cudaError_t launch_packed_fwd(const SeqShape& s, const CacheShape* c, const Rows& q, const Rows& o, const Rows& resid,

@@ -55,6 +55,18 @@ int fa_test_exp2_accurate(const float* x, float* y, int n, void* stream);
  */
 int fa_test_decode_plan(int B, int Hq, int Hkv, int Nq, int Nk, int d, int num_ctas, long long* out);
 
+/*
+ * Host only (no device call): what a launch of the packed forward (page_size =
+ * 0), or of the prompt kernel over a paged cache, lays out on a device of
+ * num_sms multiprocessors, as five integers in out[0..4]: the workspace bytes
+ * used, whether the work may be cut into runs, whether the CTAs find their
+ * units without a list, the most units times KV heads there can be, and the
+ * CTAs launched. Returns FA_OK, FA_ERR_INVALID_ARGUMENT (null out, num_sms < 1,
+ * bad shape) or FA_ERR_UNSUPPORTED, as the calls would for the shape.
+ */
+int fa_test_packed_layout(int S, int T, int Hq, int Hkv, int d, int page_size, int max_pages, int num_sms,
+                          long long* out);
+
 #ifdef __cplusplus
 }
 #endif
