@@ -61,6 +61,7 @@ constexpr int kMergeManyParts = 8;
 // a training step of 2048 tokens, 16 + 16 heads, d = 64, the additions cost more
 // than a shorter last wave gains: 58.3 -> 61.6 us), for how many waves of CTAs at
 // most, the least steps of a part, and what a CTA's start and end take, in steps.
+// (fa.h names kPartUnits: dK and dV of fewer units may not repeat bit for bit.)
 constexpr int kPartUnits = 256;
 constexpr int kPartWaves = 3;
 constexpr int kPartLeast = 6;

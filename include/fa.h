@@ -336,7 +336,11 @@ int fa_packed_fwd(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa
  * lse as fa_bwd does; o_resid (NULL or as written by the forward) sharpens
  * D_i as in fa_bwd_with_residual. dq [T][Hq][d], dk, dv [T][Hkv][d] are
  * written, not accumulated into. dq is summed over key tiles by fp32 atomic
- * additions, as in fa_bwd: its last bits may differ from run to run.
+ * additions, as in fa_bwd: its last bits may differ from run to run. So may
+ * those of dk and dv where the work is little (the sequences' tiles of 128
+ * keys, sum of ceil(n_b / 128), times Hkv fewer than 256): several CTAs may
+ * then share a key tile's queries and add up their parts. With 256 or more dk
+ * and dv repeat bit for bit.
  */
 size_t fa_packed_bwd_workspace_bytes(int S, int T, int Hq, int Hkv, int d);
 int fa_packed_bwd(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa_rows* o, const fa_rows* o_resid,

@@ -368,3 +368,27 @@ def test_a_neighbours_queries_change_no_bit(d, hq, hkv, causal):
     done()
     for o, lse in got[1:]:
         assert torch.equal(o[:300], got[0][0][:300]) and torch.equal(lse[:, :300], got[0][1][:, :300])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+def test_key_gradients_repeat_with_256_units(d, causal):
+    # 64 tiles of 128 keys times 4 KV heads: every tile's dk and dv come from one CTA. With fewer, parts are added up by
+    # several, in any order: bounds hold, the last bits may differ.
+    scale = 0.125
+    for lens, repeats in (([3800, 127, 1, 3000, 1000], True), ([700], False)):
+        tiles = sum(-(-n // 128) for n in lens)
+        assert (tiles * 4 >= 256) == repeats
+        host = inputs(lens, 8, 4, d, 530)
+        q, k, v, dout = (x.cuda() for x in host)
+        cu = offsets(lens)
+        cud = torch.from_numpy(cu).cuda()
+        o, lse, resid = fa.attention_packed_forward(q, k, v, cud, causal, scale, residual=True)
+        first = None
+        for _ in range(10):
+            grads = fa.attention_packed_backward(q, k, v, o, dout, lse, cud, causal, scale, o_resid=resid)
+            first = first or grads
+            assert not repeats or (torch.equal(grads[1], first[1]) and torch.equal(grads[2], first[2]))
+        done()
+        if not repeats:
+            backward_check(*host, grads, cu, causal, scale)
