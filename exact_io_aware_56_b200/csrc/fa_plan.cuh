@@ -57,15 +57,26 @@ constexpr int kPlanSeqs = 1024;    // sequences held in shared memory at a time
 constexpr int kPlanBuckets = 1024;
 // Units of more parts than this are merged by more warps.
 constexpr int kMergeManyParts = 8;
-// Backward: units times KV heads below which units may be cut into parts (at 304,
-// a training step of 2048 tokens, 16 + 16 heads, d = 64, the additions cost more
-// than a shorter last wave gains: 58.3 -> 61.6 us), for how many waves of CTAs at
-// most, the least steps of a part, and what a CTA's start and end take, in steps.
+// Backward: units times KV heads below which units may be cut into parts, for
+// how many waves of CTAs at most, the least steps of a part, and what a CTA's
+// start and end take, in steps. That units may be cut costs 1 to 9% even where
+// none is (the accumulators of dK and dV are zeroed, the list looks at every
+// unit twice), so not from 208 units on, where no cut was found to gain. GPU
+// time of the backward, never cut against allowed: 206 units (13100 tokens, 8 + 2
+// heads, d = 128, causal) 1229 -> 1090 us, 208 (3300, 32 + 8) 346 -> 351, 208
+// (1600, 16 + 16, no mask) 85 -> 93, 304 (2048 tokens in 8, 16 + 16, d = 64) 37 -> 40.
 // (fa.h names kPartUnits: dK and dV of fewer units may not repeat bit for bit.)
-constexpr int kPartUnits = 256;
+constexpr int kPartUnits = 208;
 constexpr int kPartWaves = 3;
 constexpr int kPartLeast = 6;
 constexpr int kPartSteps = 5;
+// Of more units than CTAs the estimate of whole units' time (mean per CTA plus
+// the longest) is too long where they differ, and parts' additions are not in
+// it: of 32 measured packs of 150 to 208 units that it would cut, the 18 that it
+// had gain 62 steps or more gained up to 35% (one lost 1.4%), the 14 that it had
+// gain 43 or less lost up to 27% (two of 1500 tokens, 16 + 8 heads, d = 128,
+// causal: 89 -> 113 us).
+constexpr int kPartGain = 48;
 // Runs are made of fewer units times KV heads than this; more units are
 // balanced well enough by taking them longest first (4 per CTA).
 constexpr int kRunUnits = 4 * 148;
@@ -329,7 +340,8 @@ __device__ void plan_block(const PlanArgs& a, PlanShared& sh) {
     __syncthreads();
     const int waves = (U * a.heads + a.part_ctas - 1) / a.part_ctas;
     const int mean = (sh.n_slots + kPartSteps * U) * a.heads / a.part_ctas;
-    int best = min(waves * (sh.most + kPartSteps), mean + sh.most + kPartSteps) * 7 / 8;  // a cut has to gain that much
+    const int whole = min(waves * (sh.most + kPartSteps), mean + sh.most + kPartSteps);
+    int best = min(whole * 7 / 8, waves > 1 ? whole - kPartGain : whole);  // a cut has to gain that much
 #pragma unroll 1
     for (int k = 1; k <= kPartWaves; ++k) {
       const int room = k * a.part_ctas / a.heads - U;  // parts of a KV head beyond one per unit

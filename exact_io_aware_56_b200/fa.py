@@ -474,7 +474,7 @@ def attention_packed_backward(q, k, v, o, dout, lse, cu_seqlens, causal: bool, s
                               workspace=None, stream=None, o_resid=None):
     """Allocates ``dq``, ``dk``, ``dv`` (and the workspace if not given) and runs :func:`fa_packed_bwd`.
 
-    ``dq`` may differ in its last bits from run to run (atomic additions); so may ``dk`` and ``dv`` of fewer than 256
+    ``dq`` may differ in its last bits from run to run (atomic additions); so may ``dk`` and ``dv`` of fewer than 208
     tiles of 128 keys times KV heads. Rows outside every sequence are not written.
     """
     return _binding().packed_bwd(q, k, v, o, o_resid, dout, lse, None, None, None, cu_seqlens, bool(causal), scale,

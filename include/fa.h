@@ -338,8 +338,8 @@ int fa_packed_fwd(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa
  * written, not accumulated into. dq is summed over key tiles by fp32 atomic
  * additions, as in fa_bwd: its last bits may differ from run to run. So may
  * those of dk and dv where the work is little (the sequences' tiles of 128
- * keys, sum of ceil(n_b / 128), times Hkv fewer than 256): several CTAs may
- * then share a key tile's queries and add up their parts. With 256 or more dk
+ * keys, sum of ceil(n_b / 128), times Hkv fewer than 208): several CTAs may
+ * then share a key tile's queries and add up their parts. With 208 or more dk
  * and dv repeat bit for bit.
  */
 size_t fa_packed_bwd_workspace_bytes(int S, int T, int Hq, int Hkv, int d);

@@ -48,3 +48,14 @@ def test_launch_fits_the_workspace(kind):
             runs += x["runs"]
             direct += x["direct"]
     assert runs > 100 and (direct > 100) == (kind == "packed")
+
+
+def test_backward_holds_key_gradients_only_where_units_may_be_cut():
+    # fp32 dK and dV (8 bytes per element) are zeroed and kept for fewer than 208 tiles of 128 keys times KV heads. (The
+    # list of units takes the 4 MB at most.)
+    for T, Hq, Hkv, d in ((1536, 32, 16, 128), (6528, 16, 4, 128), (13184, 8, 2, 64), (200 * 128, 1, 1, 64)):
+        rest = 4 * T * Hq * (d + 1)
+        assert fa.fa_packed_bwd_workspace_bytes(1, T, Hq, Hkv, d) >= rest + 8 * T * Hkv * d
+    for T, Hq, Hkv, d in ((1664, 32, 16, 128), (6656, 16, 4, 128), (13312, 8, 2, 64), (31000, 1, 1, 64)):
+        rest = 4 * T * Hq * (d + 1)
+        assert fa.fa_packed_bwd_workspace_bytes(1, T, Hq, Hkv, d) < rest + (4 << 20)
