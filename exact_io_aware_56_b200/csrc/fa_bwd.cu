@@ -37,10 +37,10 @@
 // holds the next sequence's rows, which may be anything: warp 10 zeroes them
 // in shared memory (K, V once; Q and dO of each head's last tile), after
 // which they are what rows past N are to the equal-length form, where TMA
-// fills zeros. dK and dV of such a tile are stored row by row. Fewer units
-// than SMs (few KV heads, short packs) are cut into parts of their (head,
-// query tile) iterations, whose dK and dV are added up in fp32 and converted
-// by the last kernel.
+// fills zeros. dK and dV of such a tile are stored row by row. Few units (few
+// KV heads, short packs) are cut into parts of their (head, query tile)
+// iterations where the list's estimate says that it pays; their dK and dV are
+// added up in fp32, in any order, and converted by the last kernel.
 //
 // Warp roles of bwd_main (512 threads):
 //   warps 0-3   softmax-gradient warpgroup for even query tiles (buffer 0),
